@@ -437,6 +437,131 @@ int dsa_sparse_mla_decode_noalloc(const dsa_bf16 *q, const dsa_bf16 *kv, int64_t
                                   int Hm, int W, int kv_lora, int rope_dim, float sm_scale,
                                   dsa_bf16 *out, float *lse, dsa_stream_t stream);
 
+/*
+ * g1. Append of a step's latent rows to a block-table paged latent cache, with
+ * the position rotation applied on the way (the rows that the paged MLA calls
+ * read; nothing else of the library writes them).
+ *   kv_new     bf16, n rows of kv_lora + rope_dim channels, kv_new_stride
+ *              elements apart (a multiple of 8, >= kv_lora + rope_dim: the rows
+ *              may be columns of a wider projection).
+ *   norm_w     bf16 [512], eps >= 0: the latent channels x become
+ *              x * rsqrt(mean(x^2) + eps) * norm_w; NULL: they stay x.
+ *   cos_sin    fp32 [max_pos, rope_dim]: row p holds cos of position p's
+ *              rope_dim / 2 angles, then their sines. interleaved 1: pair i is
+ *              channels (2i, 2i + 1) behind the latents; 0: (i, i + rope_dim/2).
+ *              A pair (x0, x1) becomes (x0 cos - x1 sin, x1 cos + x0 sin).
+ *              Ignored when rope_dim is 0.
+ *   tok_req, tok_pos int32 [n]: request b and position t of each new token.
+ *   block_table, max_blocks, page_size: as for dsa_sparse_mla_decode_paged; the
+ *              token's row is block_table[b, t / page_size] * page_size +
+ *              t % page_size of kv, bf16 [kv_rows, kv_lora + rope_dim].
+ *   q_rot, q   (both NULL: no queries) bf16 query heads: the rope_dim rotated
+ *              channels of head h of token i at q_rot + i * q_tok_stride +
+ *              h * q_head_stride (multiples of 8), rotated like the row's and
+ *              written to columns kv_lora .. of q, bf16 [n, Hm, kv_lora +
+ *              rope_dim]; its first kv_lora columns are not touched. q_rot may
+ *              be q + kv_lora itself (rotated in place); no other overlap.
+ * Arithmetic is fp32, rounded once to the cache's type.
+ * A token is skipped, row and heads, when its request is outside [0, B), its
+ * position negative or, with rope_dim > 0, not below max_pos; its row alone is
+ * skipped when t / page_size >= max_blocks, the block number is negative or the
+ * row is not below kv_rows. Nothing else is written. Two tokens of one call for
+ * one row race (the caller keeps them distinct).
+ * Requires kv_lora == 512, rope_dim 0 or 64, Hm <= 128 (DSA_ERR_UNSUPPORTED
+ * otherwise), page_size >= 1; queries need rope_dim > 0 and Hm >= 1. n == 0 or
+ * B == 0 launches nothing. Alignment: kv_new, norm_w, cos_sin, kv, q_rot, q 16
+ * bytes; int32 arrays 4. Nothing is read before the wait on the preceding
+ * kernel.
+ */
+int dsa_latent_append_paged(const dsa_bf16 *kv_new, int64_t kv_new_stride, const dsa_bf16 *norm_w,
+                            float eps, const float *cos_sin, int max_pos, int interleaved,
+                            const int32_t *tok_req, const int32_t *tok_pos, int n, int kv_lora,
+                            int rope_dim, const int32_t *block_table, int B, int max_blocks,
+                            int page_size, dsa_bf16 *kv, int64_t kv_rows, const dsa_bf16 *q_rot,
+                            int64_t q_tok_stride, int64_t q_head_stride, int Hm, dsa_bf16 *q,
+                            dsa_stream_t stream);
+
+/*
+ * g1 into an fp8 latent cache, the layout of dsa_sparse_mla_decode_paged_fp8:
+ *   kv8        uint8 [kv_rows, kv_lora + rope_dim]: code = E4M3(value * (1 /
+ *              kv_scale)), rounded to nearest even, saturated at +-448, NaN
+ *              kept; kv_scale finite and > 0.
+ * Everything else as dsa_latent_append_paged (the query heads stay bf16).
+ */
+int dsa_latent_append_paged_fp8(const dsa_bf16 *kv_new, int64_t kv_new_stride,
+                                const dsa_bf16 *norm_w, float eps, const float *cos_sin,
+                                int max_pos, int interleaved, const int32_t *tok_req,
+                                const int32_t *tok_pos, int n, int kv_lora, int rope_dim,
+                                const int32_t *block_table, int B, int max_blocks, int page_size,
+                                uint8_t *kv8, float kv_scale, int64_t kv_rows,
+                                const dsa_bf16 *q_rot, int64_t q_tok_stride, int64_t q_head_stride,
+                                int Hm, dsa_bf16 *q, dsa_stream_t stream);
+
+/*
+ * g2. Dense MLA over the paged latent cache for a batch whose requests share a
+ * prefix, read once for all of them ([mod.rs]: the block-table paged MLA decode
+ * that walks 0..seq_len; without a prefix it is that call).
+ *   q          bf16 [Q, Hm, kv_lora + rope_dim]: the latent columns (queries
+ *              absorbed into the latent space), then the rotated ones.
+ *   kv         bf16 [kv_rows, kv_lora + rope_dim], pages of page_size rows;
+ *              the first kv_lora columns are also the values.
+ *   prefix_table int32 [prefix_blocks], prefix_len int32 [1]: the shared
+ *              prefix's pages and its P tokens (clamped to [0, prefix_blocks *
+ *              page_size]); both may be NULL when prefix_blocks is 0 (P = 0).
+ *   block_table int32 [B, max_blocks], seq_len int32 [B]: request b's sequence
+ *              holds seq_len[b] tokens, the prefix included. Token t < P is row
+ *              t % page_size of page prefix_table[t / page_size]; token t >= P
+ *              of page block_table[b, t / page_size] (so a request's entries
+ *              below P / page_size are never read, and where P ends inside a
+ *              page the request's own page holds the rest of it).
+ *   q_req, q_pos int32 [Q]: query i sees tokens t < min(q_pos[i] + 1,
+ *              seq_len[q_req[i]]); none when q_req is outside [0, B).
+ *   Tokens whose page index is past the table, block number negative or row not
+ *   below kv_rows are ignored, and their rows never read.
+ *   For each head: z_t = sm_scale * <q[i,h,:], kv[row(t),:]> over all
+ *   kv_lora + rope_dim channels, out[i,h,:] = bf16(sum_t softmax(z)_t *
+ *   kv[row(t), :kv_lora]), lse[i,h] = log(sum_t exp(z_t)) (natural; out = 0 and
+ *   -inf when the query sees no token). lse may be NULL. Precision: the P.V
+ *   product takes the softmax weights as bf16 (an output moves by at most 2^-9
+ *   of the largest value in its channel); sums, maxima and the parts of a
+ *   sequence that are merged stay fp32.
+ *   workspace: device scratch of dsa_prefix_mla_workspace_size(Q, Hm) bytes
+ *   (16-byte aligned, no initialisation; not shared between calls that may
+ *   overlap, two captured graphs among them).
+ * The lengths live on the device: a captured call replays over other lengths,
+ * tables and a prefix of another length. Results do not depend on scheduling.
+ * Requires kv_lora == 512, rope_dim 0 or 64, Hm a multiple of 16 with 16 <= Hm
+ * <= 128, Q <= 65535, kv_rows <= INT32_MAX (DSA_ERR_UNSUPPORTED otherwise),
+ * page_size >= 1, prefix_blocks and max_blocks >= 0 (DSA_ERR_INVALID_ARG).
+ * Q == 0 launches nothing. Nothing is read before the wait on the preceding
+ * kernel.
+ */
+size_t dsa_prefix_mla_workspace_size(int Q, int Hm);
+int dsa_prefix_mla_decode_paged(const dsa_bf16 *q, const dsa_bf16 *kv, int64_t kv_rows,
+                                const int32_t *prefix_table, int prefix_blocks,
+                                const int32_t *prefix_len, const int32_t *block_table,
+                                int max_blocks, int page_size, const int32_t *seq_len,
+                                const int32_t *q_req, const int32_t *q_pos, int Q, int B, int Hm,
+                                int kv_lora, int rope_dim, float sm_scale, dsa_bf16 *out,
+                                float *lse, void *workspace, size_t workspace_bytes,
+                                dsa_stream_t stream);
+
+/*
+ * g2 over an fp8 latent cache: kv8 uint8 [kv_rows, kv_lora + rope_dim] of E4M3
+ * codes and one fp32 scale, latent value = kv_scale * E4M3(code), as for
+ * dsa_sparse_mla_decode_paged_fp8 (codes widened to bf16, which is exact; the
+ * scale applied to the logits and the output). DSA_ERR_INVALID_ARG for a
+ * kv_scale that is not finite and positive.
+ */
+int dsa_prefix_mla_decode_paged_fp8(const dsa_bf16 *q, const uint8_t *kv8, float kv_scale,
+                                    int64_t kv_rows, const int32_t *prefix_table,
+                                    int prefix_blocks, const int32_t *prefix_len,
+                                    const int32_t *block_table, int max_blocks, int page_size,
+                                    const int32_t *seq_len, const int32_t *q_req,
+                                    const int32_t *q_pos, int Q, int B, int Hm, int kv_lora,
+                                    int rope_dim, float sm_scale, dsa_bf16 *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -307,6 +307,98 @@ def sparse_mla_paged(q, kv, block_table, page_size: int, seq_len, q_req, token_i
     return sparse_mla(q, flat, req_start, q_req, token_ids, sm_scale, threads)
 
 
+def e4m3_to_f64(codes):
+    """Values of E4M3 codes (any shape) in binary64."""
+    table = np.array([f64_from_e4m3(c) for c in range(256)])
+    return table[np.asarray(codes, np.uint8)]
+
+
+def paged_row(block_table_row, page_size: int, t: int, kv_rows: int) -> int:
+    """Cache row of logical token t through one block-table row; -1 where there is none."""
+    pi = t // page_size
+    if t < 0 or pi >= len(block_table_row) or block_table_row[pi] < 0:
+        return -1
+    row = int(block_table_row[pi]) * page_size + t % page_size
+    return row if row < kv_rows else -1
+
+
+def rotate(x, angles_cos, angles_sin, interleaved: bool):
+    """Pairs (x0, x1) of the last axis turned by their angles: (x0 c - x1 s, x1 c + x0 s)."""
+    x = np.asarray(x, np.float64)
+    half = x.shape[-1] // 2
+    first = np.arange(half) * 2 if interleaved else np.arange(half)
+    second = first + (1 if interleaved else half)
+    out = np.empty_like(x)
+    out[..., first] = x[..., first] * angles_cos - x[..., second] * angles_sin
+    out[..., second] = x[..., second] * angles_cos + x[..., first] * angles_sin
+    return out
+
+
+def latent_append(kv_new, norm_w, eps: float, cos_sin, interleaved: bool, tok_req, tok_pos,
+                  block_table, page_size: int, kv_rows: int, q_rot=None):
+    """New latent rows in binary64, not rounded: ({cache row: values}, {token: rotated heads}).
+
+    kv_new [n, 512 + rope] (real numbers); norm_w [512] or None; cos_sin [max_pos, rope]
+    or None; q_rot [n, Hm, rope] or None. A token outside its request's range, the
+    table of positions or the pages is left out, row and heads, row alone for a
+    missing page.
+    """
+    kv_new = np.asarray(kv_new, np.float64)
+    rope = kv_new.shape[1] - 512
+    rows, heads = {}, {}
+    for i in range(kv_new.shape[0]):
+        b, t = int(tok_req[i]), int(tok_pos[i])
+        if not 0 <= b < len(block_table) or t < 0 or (rope and t >= len(cos_sin)):
+            continue
+        x = kv_new[i, :512]
+        y = x if norm_w is None else x / np.sqrt((x * x).mean() + np.float32(eps)) * np.asarray(norm_w, np.float64)
+        if rope:
+            c, s = np.split(np.asarray(cos_sin[t], np.float64), 2)
+            y = np.concatenate([y, rotate(kv_new[i, 512:], c, s, interleaved)])
+            if q_rot is not None:
+                heads[i] = rotate(q_rot[i], c, s, interleaved)
+        row = paged_row(block_table[b], page_size, t, kv_rows)
+        if row >= 0:
+            rows[row] = y
+    return rows, heads
+
+
+def prefix_mla(q, kv, prefix_table, prefix_len: int, block_table, page_size: int, seq_len, q_req,
+               q_pos, sm_scale: float):
+    """Dense MLA behind a shared prefix in binary64, not rounded.
+
+    q [Q, Hm, 512 + rope], kv [rows, 512 + rope] (real numbers). Query i sees the tokens
+    t < min(q_pos + 1, seq_len) of its request that have a page: t < prefix_len through
+    prefix_table, the others through the request's row of block_table. Returns
+    out [Q, Hm, 512], lse [Q, Hm], and for tolerances the softmax-weighted mean of |v|
+    [Q, Hm, 512], the largest sum of |terms| of a logit [Q, Hm] and the tokens seen [Q].
+    """
+    q, kv = np.asarray(q, np.float64), np.asarray(kv, np.float64)
+    Q, Hm, _ = q.shape
+    out, mag = np.zeros((Q, Hm, 512)), np.zeros((Q, Hm, 512))
+    lse, terms, seen = np.full((Q, Hm), -np.inf), np.zeros((Q, Hm)), np.zeros(Q, int)
+    P = min(max(int(prefix_len), 0), len(prefix_table) * page_size)
+    for i in range(Q):
+        b = int(q_req[i])
+        if not 0 <= b < len(seq_len):
+            continue
+        rows = [paged_row(prefix_table if t < P else block_table[b], page_size, t, len(kv))
+                for t in range(min(int(q_pos[i]) + 1, int(seq_len[b])))]
+        rows = [r for r in rows if r >= 0]
+        seen[i] = len(rows)
+        if not rows:
+            continue
+        k = kv[rows]
+        z = q[i] @ k.T * sm_scale
+        m = z.max(1, keepdims=True)
+        p = np.exp(z - m)
+        lse[i] = m[:, 0] + np.log(p.sum(1))
+        p /= p.sum(1, keepdims=True)
+        out[i], mag[i] = p @ k[:, :512], p @ np.abs(k[:, :512])
+        terms[i] = (np.abs(q[i]) @ np.abs(k).T).max(1) * abs(sm_scale)
+    return out, lse, mag, terms, seen
+
+
 def pipeline(wl, threads: int = 0, queries: Optional[np.ndarray] = None) -> dict:
     """All stages on a workload's raw inputs (optionally a subset of queries)."""
     qsel = np.arange(wl.Q) if queries is None else np.asarray(queries)

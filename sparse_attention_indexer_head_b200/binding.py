@@ -31,6 +31,8 @@ EXPORTS = (
     "dsa_sparse_mla_workspace_size", "dsa_sparse_mla_launch_count", "dsa_sparse_mla_decode",
     "dsa_sparse_mla_decode_noalloc", "dsa_sparse_mla_decode_paged",
     "dsa_sparse_mla_decode_paged_fp8", "dsa_noalloc_scratch_bytes",
+    "dsa_latent_append_paged", "dsa_latent_append_paged_fp8", "dsa_prefix_mla_workspace_size",
+    "dsa_prefix_mla_decode_paged", "dsa_prefix_mla_decode_paged_fp8",
 )
 
 
@@ -74,6 +76,15 @@ def _load() -> ctypes.CDLL:
                                          Z, P], I),
         "dsa_sparse_mla_decode_paged_fp8": ([P, P, F, I64, P, I, I, P, P, P, I, I, I, I, I, I, F, P,
                                              P, P, Z, P], I),
+        "dsa_latent_append_paged": ([P, I64, P, F, P, I, I, P, P, I, I, I, P, I, I, I, P, I64, P,
+                                     I64, I64, I, P, P], I),
+        "dsa_latent_append_paged_fp8": ([P, I64, P, F, P, I, I, P, P, I, I, I, P, I, I, I, P, F,
+                                         I64, P, I64, I64, I, P, P], I),
+        "dsa_prefix_mla_workspace_size": ([I, I], Z),
+        "dsa_prefix_mla_decode_paged": ([P, P, I64, P, I, P, P, I, I, P, P, P, I, I, I, I, I, F, P,
+                                         P, P, Z, P], I),
+        "dsa_prefix_mla_decode_paged_fp8": ([P, P, F, I64, P, I, P, P, I, I, P, P, P, I, I, I, I,
+                                             I, F, P, P, P, Z, P], I),
     }
     for name, (argtypes, restype) in sig.items():
         fn = getattr(L, name)
@@ -242,3 +253,56 @@ def dsa_sparse_mla_decode_paged_fp8(q, kv8, kv_scale: float, kv_rows: int, block
         _ptr(q), _ptr(kv8), float(kv_scale), kv_rows, _ptr(block_table), max_blocks, page_size,
         _ptr(seq_len), _ptr(q_req), _ptr(token_ids), Q, B, Hm, W, kv_lora, rope_dim,
         float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def dsa_latent_append_paged(kv_new, kv_new_stride: int, norm_w, eps: float, cos_sin, max_pos: int,
+                            interleaved: int, tok_req, tok_pos, n: int, kv_lora: int, rope_dim: int,
+                            block_table, B: int, max_blocks: int, page_size: int, kv, kv_rows: int,
+                            q_rot=None, q_tok_stride: int = 0, q_head_stride: int = 0, Hm: int = 0,
+                            q=None, stream=None) -> None:
+    _check("dsa_latent_append_paged", lib.dsa_latent_append_paged(
+        _ptr(kv_new), kv_new_stride, _ptr(norm_w), float(eps), _ptr(cos_sin), max_pos,
+        int(interleaved), _ptr(tok_req), _ptr(tok_pos), n, kv_lora, rope_dim, _ptr(block_table), B,
+        max_blocks, page_size, _ptr(kv), kv_rows, _ptr(q_rot), q_tok_stride, q_head_stride, Hm,
+        _ptr(q), _stream(stream)))
+
+
+def dsa_latent_append_paged_fp8(kv_new, kv_new_stride: int, norm_w, eps: float, cos_sin,
+                                max_pos: int, interleaved: int, tok_req, tok_pos, n: int,
+                                kv_lora: int, rope_dim: int, block_table, B: int, max_blocks: int,
+                                page_size: int, kv8, kv_scale: float, kv_rows: int, q_rot=None,
+                                q_tok_stride: int = 0, q_head_stride: int = 0, Hm: int = 0, q=None,
+                                stream=None) -> None:
+    _check("dsa_latent_append_paged_fp8", lib.dsa_latent_append_paged_fp8(
+        _ptr(kv_new), kv_new_stride, _ptr(norm_w), float(eps), _ptr(cos_sin), max_pos,
+        int(interleaved), _ptr(tok_req), _ptr(tok_pos), n, kv_lora, rope_dim, _ptr(block_table), B,
+        max_blocks, page_size, _ptr(kv8), float(kv_scale), kv_rows, _ptr(q_rot), q_tok_stride,
+        q_head_stride, Hm, _ptr(q), _stream(stream)))
+
+
+def dsa_prefix_mla_workspace_size(Q: int, Hm: int) -> int:
+    return int(lib.dsa_prefix_mla_workspace_size(Q, Hm))
+
+
+def dsa_prefix_mla_decode_paged(q, kv, kv_rows: int, prefix_table, prefix_blocks: int, prefix_len,
+                                block_table, max_blocks: int, page_size: int, seq_len, q_req, q_pos,
+                                Q: int, B: int, Hm: int, kv_lora: int, rope_dim: int,
+                                sm_scale: float, out, lse, workspace, workspace_bytes: int,
+                                stream=None) -> None:
+    _check("dsa_prefix_mla_decode_paged", lib.dsa_prefix_mla_decode_paged(
+        _ptr(q), _ptr(kv), kv_rows, _ptr(prefix_table), prefix_blocks, _ptr(prefix_len),
+        _ptr(block_table), max_blocks, page_size, _ptr(seq_len), _ptr(q_req), _ptr(q_pos), Q, B, Hm,
+        kv_lora, rope_dim, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def dsa_prefix_mla_decode_paged_fp8(q, kv8, kv_scale: float, kv_rows: int, prefix_table,
+                                    prefix_blocks: int, prefix_len, block_table, max_blocks: int,
+                                    page_size: int, seq_len, q_req, q_pos, Q: int, B: int, Hm: int,
+                                    kv_lora: int, rope_dim: int, sm_scale: float, out, lse,
+                                    workspace, workspace_bytes: int, stream=None) -> None:
+    _check("dsa_prefix_mla_decode_paged_fp8", lib.dsa_prefix_mla_decode_paged_fp8(
+        _ptr(q), _ptr(kv8), float(kv_scale), kv_rows, _ptr(prefix_table), prefix_blocks,
+        _ptr(prefix_len), _ptr(block_table), max_blocks, page_size, _ptr(seq_len), _ptr(q_req),
+        _ptr(q_pos), Q, B, Hm, kv_lora, rope_dim, float(sm_scale), _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace_bytes, _stream(stream)))

@@ -10,6 +10,8 @@
 #include "topk_expand.cuh"
 #include "indexer.cuh"
 #include "sparse_mla.cuh"
+#include "latent_append.cuh"
+#include "prefix_mla.cuh"
 
 // ---------------------------------------------------------------------------------------
 // Library-owned scratch for dsa_sparse_mla_decode_noalloc: the split-KV partial
@@ -227,6 +229,71 @@ int dsa_sparse_mla_decode_noalloc(const dsa_bf16 *q, const dsa_bf16 *kv, int64_t
     return dsa::sparse_mla_launch(q, kv, kv_rows, req_start, q_req, token_ids, Q, B, Hm, W,
                                   kv_lora, rope_dim, sm_scale, out, lse, scratch, need,
                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dsa_latent_append_paged(const dsa_bf16 *kv_new, int64_t kv_new_stride, const dsa_bf16 *norm_w,
+                            float eps, const float *cos_sin, int max_pos, int interleaved,
+                            const int32_t *tok_req, const int32_t *tok_pos, int n, int kv_lora,
+                            int rope_dim, const int32_t *block_table, int B, int max_blocks,
+                            int page_size, dsa_bf16 *kv, int64_t kv_rows, const dsa_bf16 *q_rot,
+                            int64_t q_tok_stride, int64_t q_head_stride, int Hm, dsa_bf16 *q,
+                            dsa_stream_t stream) {
+    const dsa::AppendArgs a{reinterpret_cast<const __nv_bfloat16 *>(kv_new), kv_new_stride,
+                            reinterpret_cast<const __nv_bfloat16 *>(norm_w), eps, cos_sin, max_pos,
+                            interleaved, tok_req, tok_pos, n, rope_dim, block_table, B, max_blocks,
+                            page_size, kv, 1.0f, kv_rows,
+                            reinterpret_cast<const __nv_bfloat16 *>(q_rot), q_tok_stride,
+                            q_head_stride, Hm, reinterpret_cast<__nv_bfloat16 *>(q)};
+    return dsa::latent_append_launch<false>(a, 1.0f, kv_lora, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dsa_latent_append_paged_fp8(const dsa_bf16 *kv_new, int64_t kv_new_stride,
+                                const dsa_bf16 *norm_w, float eps, const float *cos_sin,
+                                int max_pos, int interleaved, const int32_t *tok_req,
+                                const int32_t *tok_pos, int n, int kv_lora, int rope_dim,
+                                const int32_t *block_table, int B, int max_blocks, int page_size,
+                                uint8_t *kv8, float kv_scale, int64_t kv_rows,
+                                const dsa_bf16 *q_rot, int64_t q_tok_stride, int64_t q_head_stride,
+                                int Hm, dsa_bf16 *q, dsa_stream_t stream) {
+    const dsa::AppendArgs a{reinterpret_cast<const __nv_bfloat16 *>(kv_new), kv_new_stride,
+                            reinterpret_cast<const __nv_bfloat16 *>(norm_w), eps, cos_sin, max_pos,
+                            interleaved, tok_req, tok_pos, n, rope_dim, block_table, B, max_blocks,
+                            page_size, kv8, 1.0f, kv_rows,
+                            reinterpret_cast<const __nv_bfloat16 *>(q_rot), q_tok_stride,
+                            q_head_stride, Hm, reinterpret_cast<__nv_bfloat16 *>(q)};
+    return dsa::latent_append_launch<true>(a, kv_scale, kv_lora, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_prefix_mla_workspace_size(int Q, int Hm) { return dsa::prefix_mla_workspace_bytes(Q, Hm); }
+
+int dsa_prefix_mla_decode_paged(const dsa_bf16 *q, const dsa_bf16 *kv, int64_t kv_rows,
+                                const int32_t *prefix_table, int prefix_blocks,
+                                const int32_t *prefix_len, const int32_t *block_table,
+                                int max_blocks, int page_size, const int32_t *seq_len,
+                                const int32_t *q_req, const int32_t *q_pos, int Q, int B, int Hm,
+                                int kv_lora, int rope_dim, float sm_scale, dsa_bf16 *out,
+                                float *lse, void *workspace, size_t workspace_bytes,
+                                dsa_stream_t stream) {
+    const dsa::PrefixGeom g{prefix_table, prefix_len, block_table, seq_len, q_req, q_pos,
+                            prefix_blocks, max_blocks, page_size, Q, B, 0};
+    return dsa::prefix_mla_launch<false>(q, kv, 1.0f, kv_rows, g, Hm, kv_lora, rope_dim, sm_scale,
+                                         out, lse, workspace, workspace_bytes,
+                                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dsa_prefix_mla_decode_paged_fp8(const dsa_bf16 *q, const uint8_t *kv8, float kv_scale,
+                                    int64_t kv_rows, const int32_t *prefix_table,
+                                    int prefix_blocks, const int32_t *prefix_len,
+                                    const int32_t *block_table, int max_blocks, int page_size,
+                                    const int32_t *seq_len, const int32_t *q_req,
+                                    const int32_t *q_pos, int Q, int B, int Hm, int kv_lora,
+                                    int rope_dim, float sm_scale, dsa_bf16 *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, dsa_stream_t stream) {
+    const dsa::PrefixGeom g{prefix_table, prefix_len, block_table, seq_len, q_req, q_pos,
+                            prefix_blocks, max_blocks, page_size, Q, B, 0};
+    return dsa::prefix_mla_launch<true>(q, kv8, kv_scale, kv_rows, g, Hm, kv_lora, rope_dim,
+                                        sm_scale, out, lse, workspace, workspace_bytes,
+                                        reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,140 @@
+"""The paged append and the shared-prefix MLA on the host: refusals before anything is
+launched, and the oracle's functions pinned to closed forms."""
+import numpy as np
+import pytest
+
+import oracle as O
+from paged_helpers import cos_sin_table
+
+FAKE = 1 << 20          # a 16-byte aligned non-null address; never dereferenced on these paths
+
+
+@pytest.fixture(scope="module")
+def B():
+    from sparse_attention_indexer_head_b200 import build
+    build.build()
+    from sparse_attention_indexer_head_b200 import binding
+    return binding
+
+
+def _append(api, fp8=False, **kw):
+    a = dict(kv_new=FAKE, stride=576, norm_w=FAKE, eps=1e-6, cos_sin=FAKE, max_pos=64, interleaved=1, tok_req=FAKE,
+             tok_pos=FAKE, n=4, kv_lora=512, rope=64, table=FAKE, B=2, max_blocks=4, page=16, kv=FAKE, scale=0.5,
+             rows=128, q_rot=FAKE, qt=16 * 64, qh=64, Hm=16, q=FAKE)
+    a.update(kw)
+    head = [a[k] for k in ("kv_new", "stride", "norm_w", "eps", "cos_sin", "max_pos", "interleaved", "tok_req", "tok_pos",
+                           "n", "kv_lora", "rope", "table", "B", "max_blocks", "page", "kv")]
+    tail = [a[k] for k in ("rows", "q_rot", "qt", "qh", "Hm", "q")]
+    if fp8:
+        return api.lib.dsa_latent_append_paged_fp8(*head, a["scale"], *tail, None)
+    return api.lib.dsa_latent_append_paged(*head, *tail, None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bad,status", [
+    (dict(n=-1), 1), (dict(B=-1), 1), (dict(page=0), 1), (dict(max_blocks=-1), 1), (dict(rows=-1), 1),
+    (dict(max_pos=-1), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(stride=568), 1),
+    (dict(interleaved=2), 1), (dict(kv_new=None), 1), (dict(tok_req=None), 1), (dict(tok_pos=None), 1),
+    (dict(table=None), 1), (dict(kv=None), 1), (dict(cos_sin=None), 1), (dict(q=None), 1), (dict(q_rot=None), 1),
+    (dict(rope=0, stride=512), 1),                       # heads without a rotation
+    (dict(Hm=0), 1), (dict(qh=56), 1), (dict(qt=15 * 64), 1),
+    (dict(kv_lora=576), 2), (dict(rope=32), 2), (dict(rope=128, stride=640), 2),
+    (dict(Hm=144, qt=144 * 64), 2),
+    (dict(kv_new=FAKE + 8), 3), (dict(stride=580), 3), (dict(norm_w=FAKE + 2), 3), (dict(cos_sin=FAKE + 4), 3),
+    (dict(tok_req=FAKE + 2), 3), (dict(tok_pos=FAKE + 1), 3), (dict(table=FAKE + 2), 3), (dict(kv=FAKE + 8), 3),
+    (dict(q_rot=FAKE + 8), 3), (dict(q=FAKE + 4), 3), (dict(qh=68, qt=16 * 68), 3), (dict(qt=16 * 64 + 4), 3),
+])
+def test_append_refusals(B, bad, status, fp8):
+    assert _append(B, fp8, **bad) == status
+
+
+def test_append_scale_and_empty_calls(B):
+    for scale in (0.0, -1.0, float("inf"), float("nan")):
+        assert _append(B, True, scale=scale) == B.DSA_ERR_INVALID_ARG
+    none = dict(kv_new=None, tok_req=None, tok_pos=None, table=None, kv=None, cos_sin=None)
+    assert _append(B, n=0, **none) == B.DSA_OK
+    assert _append(B, B=0, **none) == B.DSA_OK
+    with pytest.raises(B.DsaError):
+        B.dsa_latent_append_paged(None, 576, None, 1e-6, None, 0, 1, None, None, 1, 512, 64, None, 1, 1, 0, None, 1, stream=0)
+
+
+def _mla(api, fp8=False, **kw):
+    a = dict(q=FAKE, kv=FAKE, scale=0.5, rows=64, prefix=FAKE, pb=2, plen=FAKE, table=FAKE, mb=4, page=16, seq=FAKE,
+             q_req=FAKE, q_pos=FAKE, Q=2, B=2, Hm=32, kv_lora=512, rope=64, sm=0.05, out=FAKE, lse=FAKE, ws=FAKE,
+             ws_bytes=1 << 40)
+    a.update(kw)
+    head = [a["q"], a["kv"]] + ([a["scale"]] if fp8 else [])
+    rest = [a[k] for k in ("rows", "prefix", "pb", "plen", "table", "mb", "page", "seq", "q_req", "q_pos", "Q", "B", "Hm",
+                           "kv_lora", "rope", "sm", "out", "lse", "ws", "ws_bytes")]
+    fn = api.lib.dsa_prefix_mla_decode_paged_fp8 if fp8 else api.lib.dsa_prefix_mla_decode_paged
+    return fn(*head, *rest, None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bad,status", [
+    (dict(Q=-1), 1), (dict(B=-1), 1), (dict(Hm=0), 1), (dict(page=0), 1), (dict(mb=-1), 1), (dict(pb=-1), 1),
+    (dict(rows=-1), 1), (dict(rope=-1), 1), (dict(sm=float("nan")), 1), (dict(sm=float("inf")), 1), (dict(q=None), 1),
+    (dict(kv=None), 1), (dict(prefix=None), 1), (dict(plen=None), 1), (dict(table=None), 1), (dict(seq=None), 1),
+    (dict(q_req=None), 1), (dict(q_pos=None), 1), (dict(out=None), 1),
+    (dict(kv_lora=576), 2), (dict(rope=32), 2), (dict(Hm=24), 2), (dict(Hm=144), 2), (dict(Q=65536), 2),
+    (dict(rows=1 << 31), 2),
+    (dict(q=FAKE + 8), 3), (dict(kv=FAKE + 8), 3), (dict(prefix=FAKE + 2), 3), (dict(plen=FAKE + 2), 3),
+    (dict(table=FAKE + 2), 3), (dict(seq=FAKE + 2), 3), (dict(q_req=FAKE + 2), 3), (dict(q_pos=FAKE + 2), 3),
+    (dict(out=FAKE + 8), 3), (dict(lse=FAKE + 2), 3), (dict(ws=FAKE + 8), 3),
+    (dict(ws=None), 4), (dict(ws_bytes=0), 4),
+])
+def test_prefix_mla_refusals(B, bad, status, fp8):
+    assert _mla(B, fp8, **bad) == status
+
+
+def test_prefix_mla_scale_empty_call_and_workspace(B):
+    for scale in (0.0, -1.0, float("inf"), float("nan")):
+        assert _mla(B, True, scale=scale) == B.DSA_ERR_INVALID_ARG
+    assert _mla(B, Q=0, q=None, q_req=None, out=None, ws=None) == B.DSA_OK
+    assert B.dsa_prefix_mla_workspace_size(0, 64) == 0
+    for Q, hm in [(1, 16), (64, 128), (65535, 128)]:
+        need = B.dsa_prefix_mla_workspace_size(Q, hm)
+        assert 0 < need < 64 << 20                     # it does not grow with the batch
+        assert _mla(B, Q=Q, Hm=hm, ws_bytes=need - 1) == B.DSA_ERR_WORKSPACE
+
+
+def test_oracle_rotation_is_a_complex_product():
+    rng = np.random.default_rng(0)
+    x, cs = rng.standard_normal((3, 64)), cos_sin_table(50)
+    c, s = cs[41, :32].astype(float), cs[41, 32:].astype(float)
+    turn = c + 1j * s
+    y = O.rotate(x, c, s, True)
+    np.testing.assert_allclose(y[:, 0::2] + 1j * y[:, 1::2], (x[:, 0::2] + 1j * x[:, 1::2]) * turn, rtol=1e-14, atol=1e-14)
+    y = O.rotate(x, c, s, False)
+    np.testing.assert_allclose(y[:, :32] + 1j * y[:, 32:], (x[:, :32] + 1j * x[:, 32:]) * turn, rtol=1e-14, atol=1e-14)
+
+
+def test_oracle_append_places_and_normalises():
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((3, 576))
+    table = np.array([[2, -1], [0, 1]])
+    rows, heads = O.latent_append(x, np.ones(512), 0.0, cos_sin_table(8), True, [0, 1, 0], [1, 5, 4], table, 4, 12,
+                                  np.ones((3, 2, 64)))
+    assert sorted(rows) == [5, 9] and sorted(heads) == [0, 1, 2]       # token 2's page is missing, its heads turn
+    for r in rows.values():
+        assert abs((r[:512] ** 2).mean() - 1) < 1e-12
+        # a rotation keeps lengths
+    assert abs((rows[9][512:] ** 2).sum() - (x[0, 512:] ** 2).sum()) < 1e-5
+    np.testing.assert_allclose(rows[9][:512] / rows[9][0], x[0, :512] / x[0, 0], rtol=1e-12)
+
+
+def test_oracle_prefix_mla_closed_forms():
+    kv = np.zeros((16, 512))
+    kv[:, 0] = np.arange(16)
+    q = np.zeros((3, 1, 512))
+    # equal logits: the mean of the values seen; prefix pages 3, own pages 1 and 2
+    out, lse, mag, _, seen = O.prefix_mla(q, kv, [3], 3, [[0, 1], [-1, 2]], 4, [6, 7], [0, 1, 5], [9, 5, 0], 1.0)
+    # request 0: tokens 0..2 in page 3, token 3 in its own page 0, tokens 4, 5 in page 1
+    assert seen.tolist() == [6, 5, 0]
+    assert out[0, 0, 0] == pytest.approx((12 + 13 + 14 + 3 + 4 + 5) / 6)
+    # request 1 has no page for token 3; tokens 4, 5 in page 2
+    assert out[1, 0, 0] == pytest.approx((12 + 13 + 14 + 8 + 9) / 5)
+    assert lse[0, 0] == pytest.approx(np.log(6)) and np.isneginf(lse[2]).all() and (out[2] == 0).all()
+    # one token: its value, whatever the logits
+    out, lse, *_ = O.prefix_mla(np.ones((1, 1, 512)), kv, [], 0, [[2]], 4, [1], [0], [0], 0.5)
+    assert out[0, 0, 0] == 8 and lse[0, 0] == pytest.approx(4.0)
