@@ -4,12 +4,15 @@
 // row). Plain form: one warp per (query, head), online softmax over the tokens.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include "common.cuh"
 #include "latent_append.cuh"
+#include "sparse_mla.cuh"
+#include "tc_ptx.cuh"
+#include "tma.cuh"
 
 namespace dsa {
+
+constexpr int kMaxTokens = INT32_MAX - 64;            // a unit's last token stays an int
 
 struct PrefixGeom {
     const int32_t *prefix_table;      // pages of the shared prefix
@@ -23,14 +26,14 @@ struct PrefixGeom {
     DSA_DEVINL int shared_len() const {
         if (prefix_blocks == 0) return 0;
         const long long cap = (long long)prefix_blocks * page;
-        return (int)max(0ll, min((long long)prefix_len[0], min(cap, (long long)INT32_MAX)));
+        return (int)max(0ll, min((long long)prefix_len[0], min(cap, (long long)kMaxTokens)));
     }
     // Tokens 0 .. n-1 that query q sees; no more than its pages can hold.
     DSA_DEVINL int visible(int q, int P) const {
         const int b = q_req[q];
         if (b < 0 || b >= B) return 0;
         const long long n = min((long long)q_pos[q] + 1, (long long)seq_len[b]);
-        const long long cap = max((long long)P, min((long long)max_blocks * page, (long long)INT32_MAX));
+        const long long cap = max((long long)P, min((long long)max_blocks * page, (long long)kMaxTokens));
         return (int)max(0ll, min(n, cap));
     }
     // Cache row of token t of request b, -1 where there is none.
@@ -49,55 +52,867 @@ struct PrefixGeom {
     }
 };
 
-template <bool kFp8>
-__global__ void __launch_bounds__(128)
-prefix_mla_plain_kernel(const __nv_bfloat16 *__restrict__ q, const void *__restrict__ kv,
-                        const PrefixGeom g, int Hm, int rope, float scale_log2, float out_scale,
-                        __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
-    const int lane = threadIdx.x & 31;
-    const long long task = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_launch_dependents();
-    if (task >= (long long)g.Q * Hm) return;
-    const int qi = (int)(task / Hm);
-    const int width = DSA_KV_LORA + rope;
-    const int P = g.shared_len(), n = g.visible(qi, P), b = g.q_req[qi];
-    float qv[18], o[16];
-    const __nv_bfloat16 *qr = q + (size_t)task * width;
-    for (int k = 0; k < 16; ++k) { qv[k] = __bfloat162float(qr[32 * k + lane]); o[k] = 0.f; }
-    for (int k = 0; k < 2; ++k) qv[16 + k] = rope ? __bfloat162float(qr[512 + 32 * k + lane]) : 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int t = 0; t < n; ++t) {
-        const int row = g.row(b, t, P);
-        if (row < 0) continue;
-        float v[18], z = 0.f;
-        for (int k = 0; k < 18; ++k) {
-            if (k >= 16 && !rope) { v[k] = 0.f; continue; }
-            const size_t at = (size_t)row * width + 32 * k + lane;
-            if constexpr (kFp8) {
-                uint32_t h2;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)reinterpret_cast<const uint8_t *>(kv)[at]));
-                v[k] = __half2float(__ushort_as_half((uint16_t)(h2 & 0xFFFFu)));
-            } else {
-                v[k] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(kv)[at]);
-            }
-            z = fmaf(qv[k], v[k], z);
-        }
-        for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-        z *= scale_log2;
-        const float mn = fmaxf(m, z);
-        const float al = m == -INFINITY ? 0.f : ex2(m - mn), p = z == -INFINITY ? 0.f : ex2(z - mn);
-        l = l * al + p;
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * al + p * v[k];
-        m = mn;
+// ---------------------------------------------------------------------------------------
+// Row tiles and their units of work
+// ---------------------------------------------------------------------------------------
+constexpr int kPmTile = 32;                           // tokens of a unit: one S product
+constexpr int kPmRows = 64;                           // (query, head) rows of a row tile
+constexpr int kPmGrid = 148;                          // persistent CTAs, one per SM
+constexpr int kPmMinUnits = 4;                        // units a CTA takes at least
+constexpr int kPmThreads = 512;
+constexpr int kPmQueries = 4;                         // queries a row tile holds at most
+
+// How (query, head) rows are cut into row tiles: qpt queries of Hm < 64 heads
+// each, or groups of 64 heads of one query.
+struct RowTiles {
+    int Hm, qpt, groups, count, total_rows;
+    __host__ __device__ RowTiles(int Q, int hm)
+        : Hm(hm), qpt(hm < kPmRows ? kPmRows / hm : 1), groups((hm + kPmRows - 1) / kPmRows),
+          count(qpt > 1 ? (Q + qpt - 1) / qpt : Q * groups), total_rows(Q * hm) {}
+    DSA_DEVINL int first_query(int t) const { return qpt > 1 ? t * qpt : t / groups; }
+    DSA_DEVINL int first_row(int t) const {
+        return qpt > 1 ? t * qpt * Hm : t / groups * Hm + t % groups * kPmRows;
     }
-    const float inv = l != 0.f ? out_scale / l : 0.f;
-    for (int k = 0; k < 16; ++k)
-        out[(size_t)task * 512 + 32 * k + lane] = __float2bfloat16_rn(l != 0.f ? o[k] * inv : 0.f);
-    if (lse && lane == 0) lse[task] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    DSA_DEVINL int rows(int t) const {
+        return qpt > 1 ? min(qpt * Hm, total_rows - t * qpt * Hm)
+                       : min(kPmRows, Hm - t % groups * kPmRows);
+    }
+};
+
+// The tokens a row tile walks: one segment for the shared prefix (all rows),
+// then one for each of its queries (that query's rows). With one query there is
+// one segment, its whole sequence. A query that sees only a part of the prefix
+// makes the tile walk every query on its own. Units lie at multiples of 32
+// tokens, so a unit's rows are whole pages or parts of them.
+struct TileWalk {
+    int nq, npre, units, active;
+    bool shared;
+    int vis[kPmQueries], req[kPmQueries];
+
+    DSA_DEVINL int query_units(int k, int P) const {
+        if (!shared) return (int)(((long long)vis[k] + kPmTile - 1) / kPmTile);
+        return vis[k] > P ? (int)(((long long)vis[k] + kPmTile - 1) / kPmTile) - P / kPmTile : 0;
+    }
+    DSA_DEVINL void load(const PrefixGeom &g, const RowTiles &rt, int t, int P) {
+        const int q0 = rt.first_query(t);
+        nq = min(rt.qpt, g.Q - q0);
+        shared = rt.qpt > 1 && P > 0;
+        active = 0;
+#pragma unroll
+        for (int k = 0; k < kPmQueries; ++k) {
+            vis[k] = 0;
+            req[k] = 0;
+            if (k < nq) {
+                vis[k] = g.visible(q0 + k, P);
+                req[k] = g.q_req[q0 + k];
+                active |= (vis[k] > 0 ? 1 : 0) << k;
+                shared = shared && (vis[k] == 0 || vis[k] >= P);
+            }
+        }
+        shared = shared && active != 0;
+        npre = shared ? (int)(((long long)P + kPmTile - 1) / kPmTile) : 0;
+        units = npre;
+#pragma unroll
+        for (int k = 0; k < kPmQueries; ++k)
+            if (k < nq) units += query_units(k, P);
+        units = max(units, 1);                        // a tile without tokens still writes its rows
+    }
+};
+
+// What a ring slot holds, written by its loader for the issuers and the softmax.
+struct UnitInfo {
+    int tile;                                         // row tile
+    int row0, nrows;                                  // its rows that see these tokens
+    int active;                                       // its queries that see any token
+    uint32_t valid;                                   // tokens of the unit that exist
+    int flags;                                        // kUnit*
+    int part;                                         // partial slot, -1: the tile is whole
+    int pad;
+};
+enum : int { kUnitFirst = 1, kUnitLast = 2, kUnitFresh = 4 };   // of the part; rows not yet summed
+
+struct MergeEntry { int tile, first_cta, parts, pad; };
+
+constexpr int kPmSlots = 4;                           // ring slots of one unit
+constexpr int kPmSBufs = 4;                           // S buffers in tensor memory
+constexpr uint32_t kPmSCol = 256;                     // behind O^T
+constexpr uint32_t kPmAtom = kPmSlots * kPmTile * 128;   // 64 channels of the whole ring
+constexpr uint32_t kPmSlotRows = kPmTile * 128;       // a slot's rows within an atom
+constexpr uint32_t kPmPBytes = kPmRows * 128;         // two P buffers, the halves of 128-byte rows
+static_assert(kPmSCol + kPmSBufs * kPmTile <= 512, "tensor memory columns");
+
+struct PmCtl {
+    uint64_t kv_full[kPmSlots], kv_empty[kPmSlots];
+    uint64_t s_full[kPmSBufs], s_empty[kPmSBufs];
+    uint64_t p_full[2], p_empty[2];
+    uint64_t o_done, o_final, q_full, fin;
+    UnitInfo unit[kPmSlots];
+    float alpha[kPmRows], linv[kPmRows];
+    long long warp_sum[16];
+    long long total, per, begin;
+    int first_tile, first_unit, first_units;
+    uint32_t tmem_base;
+    volatile int abort;
+};
+
+template <int kWidth>
+struct PmSmem {
+    static constexpr int kAtoms = kWidth / 64;
+    static constexpr uint32_t kQ = 0;                               // kAtoms x [64 rows x 128 B]
+    static constexpr uint32_t kKV = kAtoms * kPmRows * 128;         // kAtoms x [128 rows x 128 B]
+    static constexpr uint32_t kP = kKV + kAtoms * kPmAtom;
+    static constexpr uint32_t kCtl = kP + kPmPBytes;
+    static constexpr int kBytes = (int)kCtl + (int)sizeof(PmCtl) + 1024;   // + alignment slack
+};
+static_assert(PmSmem<576>::kBytes <= 232448, "shared memory per block");
+static_assert(65535 * 2 <= (int)(kPmPBytes / 8) * kPmThreads, "block sums hold every row tile");
+
+DSA_DEVINL bool pm_wait(PmCtl *ctl, uint64_t *bar, uint32_t parity) {
+    if (ctl->abort) return false;
+    if (!mbar_wait(bar, parity)) {
+        ctl->abort = 1;
+        return false;
+    }
+    return true;
 }
 
-inline size_t prefix_mla_workspace_bytes(int Q, int Hm) { return Q > 0 && Hm > 0 ? 16 : 0; }
+// One lane of a converged warp, chosen so that the compiler knows it is one:
+// descriptors then stay in uniform registers (an `if (lane == 0)` costs about
+// 155 cycles a tcgen05.mma, this about 30).
+DSA_DEVINL bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+DSA_DEVINL long long warp_inclusive_sum(long long v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// The plan: units of all row tiles in order, cut into equal ranges of `per`
+// units, one a CTA (a row tile split over CTAs leaves partial results; a CTA
+// leaves at most two, one of its first and one of its last row tile). Every CTA
+// works it out from the lengths on the device, so nothing depends on the host's
+// bounds, and ragged batches load every SM alike. block_sum: shared scratch, one
+// sum for every 512 row tiles.
+DSA_DEVINL void pm_plan(PmCtl *ctl, long long *block_sum, const PrefixGeom &g, const RowTiles &rt, int P) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nb = (rt.count + kPmThreads - 1) / kPmThreads;
+    for (int k = tid; k < nb; k += kPmThreads) block_sum[k] = 0;
+    __syncthreads();
+    TileWalk w;
+    int units = 0;
+    for (int k = 0; k < nb; ++k) {
+        const int t = k * kPmThreads + tid;
+        units = 0;
+        if (t < rt.count) {
+            w.load(g, rt, t, P);
+            units = w.units;
+        }
+        long long s = units;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0 && s)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&block_sum[k]), (unsigned long long)s);
+    }
+    __syncthreads();
+    long long total = 0;
+    for (int k = 0; k < nb; ++k) total += block_sum[k];
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kPmMinUnits);
+    const long long begin = per * blockIdx.x;
+    if (tid == 0) {
+        ctl->total = total;
+        ctl->per = per;
+        ctl->begin = begin;
+    }
+    if (begin < total) {
+        long long base = 0;
+        int kb = 0;
+        while (base + block_sum[kb] <= begin) base += block_sum[kb++];
+        if (nb > 1) {
+            const int t = kb * kPmThreads + tid;
+            units = 0;
+            if (t < rt.count) {
+                w.load(g, rt, t, P);
+                units = w.units;
+            }
+        }
+        const long long inc = warp_inclusive_sum(units, lane);
+        if (lane == 31) ctl->warp_sum[warp] = inc;
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) base += ctl->warp_sum[k];
+        const long long lo = base + inc - units;
+        if (units > 0 && lo <= begin && begin < lo + units) {
+            ctl->first_tile = kb * kPmThreads + tid;
+            ctl->first_unit = (int)(begin - lo);
+            ctl->first_units = units;
+        }
+    }
+    __syncthreads();
+}
+
+// kv: kv_rows rows of kWidth bf16, or E4M3 bytes (kFp8; widened to bf16, which
+// is exact). box_rows: rows of a box of kv_map, 0 where pages allow none.
+template <bool kFp8, int kWidth>
+__global__ void __launch_bounds__(kPmThreads, 1)
+prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
+                  const __nv_bfloat16 *__restrict__ q, const void *__restrict__ kv,
+                  const PrefixGeom g, int Hm, float scale_log2, float out_scale,
+                  float *__restrict__ part, float2 *__restrict__ part_ml,
+                  MergeEntry *__restrict__ merge, __nv_bfloat16 *__restrict__ out,
+                  float *__restrict__ lse) {
+    using S = PmSmem<kWidth>;
+    constexpr int kAtoms = S::kAtoms;
+    extern __shared__ uint8_t pm_smem_raw[];
+    const uint32_t raw = smem_u32(pm_smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;           // 128B-swizzle atoms need 1 KB
+    uint8_t *gbase = pm_smem_raw + (base - raw);
+    PmCtl *ctl = reinterpret_cast<PmCtl *>(gbase + S::kCtl);
+    const uint32_t sQ = base + S::kQ, sKV = base + S::kKV, sP = base + S::kP;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const RowTiles rt(g.Q, Hm);
+
+    if (warp == 0) {
+        tc::tmem_alloc(&ctl->tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 32) {
+        for (int i = 0; i < kPmSlots; ++i) {
+            mbar_init(&ctl->kv_full[i], 4 * 32 + 4);  // four warps' lanes' copies + a word from each warp
+            mbar_init(&ctl->kv_empty[i], 1);
+        }
+        for (int i = 0; i < kPmSBufs; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->s_empty[i], 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->p_full[i], 128);
+            mbar_init(&ctl->p_empty[i], 1);
+        }
+        mbar_init(&ctl->o_done, 1);
+        mbar_init(&ctl->o_final, 1);
+        mbar_init(&ctl->q_full, 128);
+        mbar_init(&ctl->fin, 2);
+        ctl->abort = 0;
+        fence_mbarrier_init();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+    pdl_wait();                       // queries, lengths and cache rows may come from the predecessor
+    pdl_launch_dependents();
+
+    const int P = g.shared_len();
+    pm_plan(ctl, reinterpret_cast<long long *>(gbase + S::kP), g, rt, P);
+    const int n = (int)min((long long)INT32_MAX, max(0ll, min(ctl->per, ctl->total - ctl->begin)));
+    const bool by_tile = rt.count <= kPmGrid;
+    if (!by_tile && tid == 0) {
+        // merge entries by CTA: the second CTA of a split row tile holds it
+        MergeEntry e{-1, 0, 0, 0};
+        if (n > 0 && ctl->first_unit > 0) {
+            const long long tb = ctl->begin - ctl->first_unit;
+            const int cf = (int)(tb / ctl->per), cl = (int)((tb + ctl->first_units - 1) / ctl->per);
+            if (cf == (int)blockIdx.x - 1) e = MergeEntry{ctl->first_tile, cf, cl - cf + 1, 0};
+        }
+        merge[blockIdx.x] = e;
+    }
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ S issuer
+        // S(c)[64 rows x 32 tokens] = Q K^T, kWidth / 16 K-steps.
+        constexpr uint32_t idS = tc::idesc_bf16(64, kPmTile, false, false);
+        bool ok = true;
+        int parts = 0;
+        for (int c = 0; ok && c < n; ++c) {
+            const int slot = c % kPmSlots, sb = c % kPmSBufs;
+            ok = pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
+            if (ok && (ctl->unit[slot].flags & kUnitFirst)) ok = pm_wait(ctl, &ctl->q_full, parts++ & 1);
+            if (ok && c >= kPmSBufs) ok = pm_wait(ctl, &ctl->s_empty[sb], ((c / kPmSBufs) - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::fence_proxy_async_smem();                 // the slot may have been written by cp.async
+            if (elect_one()) {
+                const uint32_t d = tmem + kPmSCol + (uint32_t)(sb * kPmTile);
+                const uint64_t a0 = tc::desc_sw128(sQ, 16, 1024);
+                const uint64_t b0 = tc::desc_sw128(sKV + slot * kPmSlotRows, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < kWidth / 16; ++kk)
+                    tc::mma_bf16_ss(d, a0 + (uint64_t)(((kk >> 2) * kPmRows * 128 + (kk & 3) * 32) >> 4),
+                                    b0 + (uint64_t)(((kk >> 2) * kPmAtom + (kk & 3) * 32) >> 4), idS,
+                                    kk > 0 ? 1u : 0u);
+                tc::mma_commit(&ctl->s_full[sb]);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) tc::mma_commit(&ctl->fin);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ PV issuer
+        // O^T[128 b .. + 127][the unit's rows] += V^T P^T for the four 128-channel
+        // blocks b: rows are the N dimension, so a unit that one query sees touches
+        // that query's columns alone (a NaN among its values reaches no other).
+        bool ok = true;
+        for (int c = 0; ok && c < n; ++c) {
+            const int slot = c % kPmSlots, pb = c & 1;
+            ok = pm_wait(ctl, &ctl->p_full[pb], (c >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::fence_proxy_async_smem();                 // the slot may have been written by cp.async
+            const int row0 = __shfl_sync(0xffffffffu, ctl->unit[slot].row0, 0);
+            const int nrows = __shfl_sync(0xffffffffu, ctl->unit[slot].nrows, 0);
+            const int flags = __shfl_sync(0xffffffffu, ctl->unit[slot].flags, 0);
+            if (elect_one()) {
+                const uint32_t id = (tc::idesc_bf16(128, 0, true, false)) | ((uint32_t)(nrows >> 3) << 17);
+                // V^T: MN-major, 64-channel atoms kPmAtom apart, 8-token groups 1 KB apart
+                const uint64_t a0 = tc::desc_sw128(sKV + slot * kPmSlotRows, kPmAtom, 1024);
+                // P^T: K-major, 128-byte rows (this buffer's half), 8-row groups 1 KB apart
+                const uint64_t b0 = tc::desc_sw128(sP + row0 * 128 + pb * 64, 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < kPmTile / 16; ++ks)
+#pragma unroll
+                    for (int blk = 0; blk < 4; ++blk)
+                        tc::mma_bf16_ss(tmem + (uint32_t)(blk * kPmRows + row0),
+                                        a0 + (uint64_t)((blk * 2 * kPmAtom + ks * 2048) >> 4),
+                                        b0 + (uint64_t)((ks * 32) >> 4), id,
+                                        (ks > 0 || !(flags & kUnitFresh)) ? 1u : 0u);
+                tc::mma_commit(&ctl->kv_empty[slot]);
+                tc::mma_commit(&ctl->p_empty[pb]);
+                tc::mma_commit(&ctl->o_done);
+                if (flags & kUnitLast) tc::mma_commit(&ctl->o_final);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) tc::mma_commit(&ctl->fin);
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------------ loaders
+        // Two groups of four warps fill alternate units. Lane l of every warp finds
+        // the cache row of the unit's token l. Where the 32 rows are whole boxes of
+        // the tensor map (pages that are a multiple of 16 rows, away from the ends
+        // of a segment) one thread brings them by TMA; else warp i of the group
+        // copies rows 8i .. 8i+7 in 16-byte pieces, zero-filled where there is no
+        // token: what lies behind a sequence may hold anything, and a weight of 0
+        // times a NaN would not be 0.
+        const int grp = (warp - 8) >> 2, sub = (warp - 8) & 3;
+        TileWalk w;
+        int tile = n > 0 ? ctl->first_tile : 0, u = n > 0 ? ctl->first_unit : 0;
+        int part_begin = u;                               // the part's first unit in its tile
+        if (n > 0) w.load(g, rt, tile, P);
+        long long global_unit = ctl->begin;
+        int left = n;                                     // units from the current one on
+
+        // describe the current unit; returns the row of this lane's token
+        auto describe = [&](UnitInfo &info) -> int {
+            int seg_unit = u, k = -1, s0 = 0, s1 = P, rows0 = 0, rowsn = kPmRows, b = 0;
+            if (u >= w.npre) {
+                seg_unit = u - w.npre;
+                k = 0;
+#pragma unroll
+                for (int i = 0; i < kPmQueries - 1; ++i) {
+                    const int nu = i < w.nq ? w.query_units(i, P) : 0;
+                    if (k == i && i + 1 < w.nq && seg_unit >= nu) {
+                        seg_unit -= nu;
+                        k = i + 1;
+                    }
+                }
+                s0 = w.shared ? P : 0;
+                s1 = w.vis[0];
+                b = w.req[0];
+#pragma unroll
+                for (int i = 1; i < kPmQueries; ++i)
+                    if (k == i) { s1 = w.vis[i]; b = w.req[i]; }
+                if (rt.qpt > 1) { rows0 = k * Hm; rowsn = Hm; }
+            }
+            const int tok0 = (k < 0 ? 0 : s0 / kPmTile * kPmTile) + seg_unit * kPmTile;
+            const int part_last = min(w.units, u + left) - 1;
+            const bool none = w.active == 0;              // no query sees a token: an empty unit
+            if (none) { rows0 = 0; rowsn = kPmRows; }
+            info.tile = tile;
+            info.row0 = rows0;
+            info.nrows = rowsn;
+            info.active = w.active;
+            const bool pre_seen = w.shared && part_begin < w.npre;
+            const bool fresh = u == part_begin || (k >= 0 && seg_unit == 0 && !pre_seen);
+            info.flags = (u == part_begin ? kUnitFirst : 0) | (u == part_last ? kUnitLast : 0) |
+                         (fresh ? kUnitFresh : 0);
+            const bool whole = part_begin == 0 && part_last == w.units - 1;
+            info.part = whole ? -1 : 2 * (int)blockIdx.x + (part_begin == 0 ? 1 : 0);
+            info.pad = 0;
+            const int t = tok0 + lane;
+            int row = -1;
+            if (!none && t >= s0 && t < s1) row = g.row(b, t, P);
+            info.valid = __ballot_sync(0xffffffffu, row >= 0);
+            if (by_tile && u == 0 && sub == 0 && lane == 0) {
+                // merge entries by row tile, left by the CTA that begins it
+                const int cf = (int)(global_unit / ctl->per);
+                const int cl = (int)((global_unit + w.units - 1) / ctl->per);
+                merge[tile] = MergeEntry{tile, cf, cl - cf + 1, 0};
+            }
+            return row;
+        };
+        // one unit forward; false behind the last
+        auto advance = [&]() -> bool {
+            if (--left <= 0) return false;
+            ++global_unit;
+            if (++u >= w.units) {
+                u = 0;
+                part_begin = 0;
+                w.load(g, rt, ++tile, P);
+            }
+            return true;
+        };
+
+        bool more = n > 0;
+        if (grp == 1) more = more && advance();
+        UnitInfo info, next_info;
+        int row = -1, next_row = -1;
+        if (more) row = describe(info);
+        for (int c = grp; more; c += 2) {
+            const int slot = c % kPmSlots;
+            const bool next = advance() && advance();
+            if (next) next_row = describe(next_info);     // its page lookups run behind this unit's copies
+            const uint32_t dst0 = sKV + slot * kPmSlotRows;
+            bool ok = true;
+            if constexpr (!kFp8) {
+                if (c >= kPmSlots) ok = pm_wait(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                bool boxes = box_rows > 0 && info.valid == 0xffffffffu;
+                if (boxes) {
+                    const int first = __shfl_sync(0xffffffffu, row, lane & ~(box_rows - 1));
+                    boxes = __all_sync(0xffffffffu, row == first + (lane & (box_rows - 1)));
+                }
+                if (boxes) {
+                    const int row_b = __shfl_sync(0xffffffffu, row, box_rows & 31);   // the second box
+                    if (sub == 0) {
+                        if (lane == 0) {
+                            ctl->unit[slot] = info;
+                            mbar_arrive_expect_tx(&ctl->kv_full[slot], kPmTile * kWidth * 2);
+                            for (int a = 0; a < kAtoms; ++a) {
+                                tma_load_2d(dst0 + a * kPmAtom, &kv_map, a * 64, row, &ctl->kv_full[slot]);
+                                if (box_rows == 16)
+                                    tma_load_2d(dst0 + a * kPmAtom + 16 * 128, &kv_map, a * 64, row_b,
+                                                &ctl->kv_full[slot]);
+                            }
+                        }
+                    } else if (lane == 0) {
+                        mbar_arrive(&ctl->kv_full[slot]);
+                    }
+                    __syncwarp();
+                    mbar_arrive(&ctl->kv_full[slot]);
+                } else {
+                    const auto *kvb = reinterpret_cast<const __nv_bfloat16 *>(kv);
+#pragma unroll
+                    for (int rr = 0; rr < 8; ++rr) {
+                        const int r = 8 * sub + rr;
+                        const int src_row = __shfl_sync(0xffffffffu, row, r);
+                        const __nv_bfloat16 *src = src_row >= 0 ? kvb + (size_t)src_row * kWidth : q;   // q: never read
+                        const uint32_t nb = src_row >= 0 ? 16u : 0u;
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const int cc = lane + 32 * hh;                    // 16-byte piece of the row
+                            tc::cp_async16_zfill(dst0 + (cc >> 3) * kPmAtom + r * 128 + (((cc & 7) ^ (r & 7)) << 4),
+                                                 src_row >= 0 ? src + cc * 8 : src, nb);
+                        }
+                    }
+                    if constexpr (kWidth > DSA_KV_LORA) {
+                        // the rotated channels: eight pieces a row, four rows a pass
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const int r = 8 * sub + 4 * rr + (lane >> 3), cc = lane & 7;
+                            const int src_row = __shfl_sync(0xffffffffu, row, r);
+                            const __nv_bfloat16 *src =
+                                src_row >= 0 ? kvb + (size_t)src_row * kWidth + DSA_KV_LORA + cc * 8 : q;
+                            tc::cp_async16_zfill(dst0 + (kAtoms - 1) * kPmAtom + r * 128 + ((cc ^ (r & 7)) << 4),
+                                                 src, src_row >= 0 ? 16u : 0u);
+                        }
+                    }
+                    if (lane == 0) {
+                        if (sub == 0) ctl->unit[slot] = info;
+                        mbar_arrive(&ctl->kv_full[slot]);
+                    }
+                    tc::cp_async_arrive_noinc(&ctl->kv_full[slot]);
+                }
+            } else {
+                // E4M3 rows: 16-byte pieces (16 channels) of the warp's 8 rows, all loads
+                // in flight before the slot is free, then widened to bf16 exactly.
+                constexpr int kPieces = kWidth / 16;                       // 32 or 36 a row
+                constexpr int kLoads = (8 * kPieces + 31) / 32;            // 8 or 9 a lane
+                const auto *kv8 = reinterpret_cast<const uint8_t *>(kv);
+                uint4 raw16[kLoads];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    // pieces 0..31 of row i, then pieces 32..35 of the eight rows
+                    const int r = 8 * sub + (i < 8 ? i : lane >> 2);
+                    const int pc = i < 8 ? lane : 32 + (lane & 3);
+                    const int src_row = __shfl_sync(0xffffffffu, row, r);
+                    raw16[i] = src_row >= 0 ? ldg_nc_v4(kv8 + (size_t)src_row * kWidth + 16 * pc)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (c >= kPmSlots) ok = pm_wait(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int r = 8 * sub + (i < 8 ? i : lane >> 2);
+                    const int pc = i < 8 ? lane : 32 + (lane & 3);
+                    const uint32_t x[4] = {raw16[i].x, raw16[i].y, raw16[i].z, raw16[i].w};
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int cc = 2 * pc + hh;                        // 16-byte piece of the bf16 row
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         dst0 + (cc >> 3) * kPmAtom + r * 128 + (((cc & 7) ^ (r & 7)) << 4)),
+                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh] & 0xFFFFu))),
+                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh] >> 16))),
+                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh + 1] & 0xFFFFu))),
+                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh + 1] >> 16)))
+                                     : "memory");
+                    }
+                }
+                tc::fence_proxy_async_smem();               // generic stores -> tensor-core reads
+                if (lane == 0) {
+                    if (sub == 0) ctl->unit[slot] = info;
+                    mbar_arrive(&ctl->kv_full[slot]);
+                }
+                mbar_arrive(&ctl->kv_full[slot]);
+            }
+            more = next;
+            info = next_info;
+            row = next_row;
+        }
+        tc::cp_async_wait_all();          // nothing of this warp in flight past here
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------------ softmax (warps 4-7)
+        // S is read with the 16x64b tensor-memory shape: thread t of warp 4+wq holds
+        // row hh = 16 wq + (t>>2) + 8 (t&1) and the unit's tokens of parity
+        // par = (t>>1)&1; its partner t^2 holds the other parity of the same row.
+        const int wq = warp - 4, wtid = tid - 128;
+        const int hh = 16 * wq + (lane >> 2) + 8 * (lane & 1);
+        const int par = (lane >> 1) & 1;
+        const bool owner = par == 0;          // writes the row's values
+        const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
+        const int hq = rt.qpt > 1 ? hh / Hm : 0;   // the row's query within its tile
+        float m_used = -INFINITY, l = 0.f;
+        int parts = 0;
+        bool failed = false;
+
+        // Q rows of a row tile into the swizzled K-major layout
+        auto load_q = [&](int tile) {
+            const int row0 = rt.first_row(tile), nr = rt.rows(tile);
+            constexpr int kPieces = kWidth / 8;
+            for (int x = wtid; x < kPmRows * kPieces; x += 128) {
+                const int r = x / kPieces, cc = x % kPieces;
+                const uint32_t dst = sQ + (cc >> 3) * (kPmRows * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
+                if (r < nr)
+                    tc::cp_async16(dst, q + (size_t)(row0 + r) * kWidth + cc * 8);
+                else
+                    tc::st_shared_zero16(dst);
+            }
+        };
+        auto release_q = [&]() {
+            tc::cp_async_wait_all();
+            tc::fence_proxy_async_smem();
+            mbar_arrive(&ctl->q_full);
+        };
+        int next_tile = n > 0 ? ctl->first_tile : 0;
+        if (n > 0) {
+            load_q(next_tile++);
+            release_q();
+        }
+        for (int c = 0; c < n; ++c) {
+            const int slot = c % kPmSlots, pb = c & 1, sb = c % kPmSBufs;
+            bool bad = !pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
+            const UnitInfo info = ctl->unit[slot];
+            bad = bad || !pm_wait(ctl, &ctl->s_full[sb], (c / kPmSBufs) & 1);
+            tc::fence_after_sync();
+            uint32_t sr[16];                              // tokens par + 2i
+            tc::tmem_ld16x64b_x16(tl + kPmSCol + (uint32_t)(sb * kPmTile), sr);
+            tc::tmem_wait_ld();
+            tc::fence_before_sync();
+            mbar_arrive(&ctl->s_empty[sb]);
+
+            const bool mine = hh >= info.row0 && hh < info.row0 + info.nrows &&
+                              ((info.active >> hq) & 1);
+            const uint32_t vm = mine ? info.valid >> par : 0u;
+            float z[16];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                z[i] = ((vm >> (2 * i)) & 1) ? __uint_as_float(sr[i]) * scale_log2 : -INFINITY;
+                mx = fmaxf(mx, z[i]);
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            float alpha = 1.f;
+            bool moved = false;
+            if (mx > m_used + kLazyRescale) {
+                moved = m_used != -INFINITY;          // nothing summed before: nothing to rescale
+                alpha = ex2(m_used - mx);
+                m_used = mx;
+            }
+            float psum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                z[i] = z[i] == -INFINITY ? 0.f : ex2(z[i] - m_used);
+                psum += z[i];        // fp32 weights: the row sum and lse stay exact to fp32
+            }
+            psum += __shfl_xor_sync(0xffffffffu, psum, 2);
+            l = fmaf(l, alpha, psum);
+            if (owner) ctl->alpha[hh] = alpha;
+            // bf16 P row: this thread packs tokens 16 par .. 16 par + 15, taking the
+            // other parity from its partner.
+            uint32_t pk[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float recv = __shfl_xor_sync(0xffffffffu, par ? z[k] : z[k + 8], 2);
+                pk[k] = par ? pack_bf16x2(recv, z[k + 8]) : pack_bf16x2(z[k], recv);
+            }
+            bad = bad || (c >= 2 && !pm_wait(ctl, &ctl->p_empty[pb], ((c >> 1) - 1) & 1));
+            // One barrier a unit; a second only when some row rescales or a wait failed.
+            const bool first = (info.flags & kUnitFirst) != 0;
+            bool need = false;
+            if (tc::named_bar_or(2, 128, bad || (!first && moved))) {
+                if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
+                need = true;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c16 = 4 * pb + 2 * par + k;     // 16-byte piece of the 128-byte row
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 sP + hh * 128 + ((c16 ^ (hh & 7)) << 4)),
+                             "r"(pk[4 * k]), "r"(pk[4 * k + 1]), "r"(pk[4 * k + 2]), "r"(pk[4 * k + 3])
+                             : "memory");
+            }
+            if (need) {
+                // O^T columns of rescaled rows times alpha, after PV(c-1) has landed
+                bad = !pm_wait(ctl, &ctl->o_done, (c - 1) & 1);
+                if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int blk = 0; blk < 8; ++blk) {
+                    uint32_t o[32];
+                    const uint32_t ta = tl + (blk >> 1) * 64 + (blk & 1) * 32;
+                    tc::tmem_ld32(ta, o);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * ctl->alpha[(blk & 1) * 32 + j]);
+                    tc::tmem_st32(ta, o);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+            }
+            tc::fence_proxy_async_smem();
+            mbar_arrive(&ctl->p_full[pb]);
+            if (!(info.flags & kUnitLast)) continue;
+
+            // -------------------------------------------------------------- end of a part
+            // Every S of this part is done: the next row tile's queries are loaded while
+            // the last PV runs, and its products start behind this part's output.
+            const bool more = c + 1 < n;
+            if (more) load_q(next_tile++);
+            bad = !pm_wait(ctl, &ctl->o_final, parts++ & 1);
+            if (owner) ctl->linv[hh] = l != 0.f ? out_scale / l : 0.f;
+            if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
+            if (more) release_q();
+            tc::fence_after_sync();
+            const int nr = rt.rows(info.tile);
+            const size_t row0 = (size_t)rt.first_row(info.tile);
+            if (info.part < 0) {
+                if (lse && owner && hh < nr)
+                    lse[row0 + hh] = l != 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                // Lanes 2i and 2i+1 hold channels L, L+1: the even lane writes both
+                // channels of row j, the odd lane those of row j+1.
+                const bool odd = lane & 1;
+                __nv_bfloat16 *ob = out + row0 * kL;
+#pragma unroll 1
+                for (int blk = 0; blk < 8; ++blk) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tl + (blk >> 1) * 64 + (blk & 1) * 32, o);
+                    tc::tmem_wait_ld();
+                    const int L2 = (blk >> 1) * 128 + 32 * wq + (lane & ~1);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float x = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? o[j] : o[j + 1]), 1);
+                        const float y = __uint_as_float(odd ? o[j + 1] : o[j]);
+                        const int r = (blk & 1) * 32 + j + (odd ? 1 : 0);
+                        const float inv = ctl->linv[r];
+                        // a row that saw nothing is 0 whatever its column holds
+                        const float lo = inv != 0.f ? (odd ? x : y) * inv : 0.f;
+                        const float hi = inv != 0.f ? (odd ? y : x) * inv : 0.f;
+                        if (r < nr) *reinterpret_cast<uint32_t *>(ob + (size_t)r * kL + L2) = pack_bf16x2(lo, hi);
+                    }
+                }
+            } else {
+                if (owner) part_ml[(size_t)info.part * kPmRows + hh] = make_float2(m_used, l);
+                float *po = part + (size_t)info.part * kPmRows * kL;
+#pragma unroll 1
+                for (int blk = 0; blk < 8; ++blk) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tl + (blk >> 1) * 64 + (blk & 1) * 32, o);
+                    tc::tmem_wait_ld();
+                    const int L = (blk >> 1) * 128 + 32 * wq + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int r = (blk & 1) * 32 + j;
+                        if (r < nr) po[(size_t)r * kL + L] = __uint_as_float(o[j]);
+                    }
+                }
+            }
+            tc::fence_before_sync();
+            tc::named_bar_sync(2, 128);       // linv is read before the next part writes it
+            m_used = -INFINITY;
+            l = 0.f;
+        }
+        (void)failed;
+        tc::cp_async_wait_all();
+    }
+
+    // Every MMA of this CTA has completed before tensor memory is released.
+    __syncwarp();
+    if (warp == 0) (void)mbar_wait(&ctl->fin, 0);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// Row tiles that were split: entry blockIdx.x, kRowsPerBlock rows a block. 512
+// threads are four groups of 128 (4 channels a thread), each merging every
+// fourth part in order; the groups are merged in order (deterministic).
+constexpr int kMergeGroups = 4;
+
+__global__ void __launch_bounds__(kMergeGroups * 128)
+prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict__ part_ml,
+                        const MergeEntry *__restrict__ merge, int Q, int Hm, int rows_per_block,
+                        float out_scale, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+    __shared__ float4 so[kMergeGroups][128];
+    __shared__ float2 sml[kMergeGroups];
+    const int grp = threadIdx.x >> 7, ct = threadIdx.x & 127;
+    pdl_wait();
+    pdl_launch_dependents();
+    const MergeEntry e = merge[blockIdx.x];
+    const RowTiles rt(Q, Hm);
+    if (e.tile < 0 || e.tile >= rt.count || e.parts <= 1) return;
+    if (e.first_cta < 0 || e.parts > kPmGrid || e.first_cta + e.parts > kPmGrid) return;
+    const int nr = rt.rows(e.tile), row0 = rt.first_row(e.tile);
+    const int r1 = min(nr, (int)(blockIdx.y + 1) * rows_per_block);
+    for (int r = blockIdx.y * rows_per_block; r < r1; ++r) {
+        auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * e.first_cta + 1 : 2 * (e.first_cta + i)); };
+        float M = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kU = 4;
+        for (int i0 = grp; i0 < e.parts; i0 += kU * kMergeGroups) {
+            float2 ml[kU];
+            float4 v[kU];
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+                const int i = i0 + k * kMergeGroups;
+                const bool in = i < e.parts;
+                ml[k] = in ? part_ml[slot(i) * kPmRows + r] : make_float2(-INFINITY, 0.f);
+                v[k] = in ? reinterpret_cast<const float4 *>(part + (slot(i) * kPmRows + r) * kL)[ct]
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float Mn = M;
+#pragma unroll
+            for (int k = 0; k < kU; ++k) Mn = fmaxf(Mn, ml[k].x);
+            const float keep = l != 0.f ? ex2(M - Mn) : 0.f;
+            M = Mn;
+            if (l != 0.f) { l *= keep; o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep; }
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+                if (ml[k].y == 0.f) continue;         // a part without tokens: its row holds nothing
+                const float wt = ex2(ml[k].x - M);
+                l = fmaf(ml[k].y, wt, l);
+                o.x = fmaf(v[k].x, wt, o.x);
+                o.y = fmaf(v[k].y, wt, o.y);
+                o.z = fmaf(v[k].z, wt, o.z);
+                o.w = fmaf(v[k].w, wt, o.w);
+            }
+        }
+        so[grp][ct] = o;
+        if (ct == 0) sml[grp] = make_float2(M, l);
+        __syncthreads();
+        if (grp == 0) {
+            float Ma = M;
+#pragma unroll
+            for (int k = 1; k < kMergeGroups; ++k) Ma = fmaxf(Ma, sml[k].x);
+            float lt = 0.f;
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMergeGroups; ++k) {
+                const float2 ml = sml[k];
+                if (ml.y == 0.f) continue;
+                const float wt = ex2(ml.x - Ma);
+                const float4 v = so[k][ct];
+                lt = fmaf(ml.y, wt, lt);
+                t.x = fmaf(v.x, wt, t.x);
+                t.y = fmaf(v.y, wt, t.y);
+                t.z = fmaf(v.z, wt, t.z);
+                t.w = fmaf(v.w, wt, t.w);
+            }
+            const float inv = lt != 0.f ? out_scale / lt : 0.f;
+            uint2 pk;
+            pk.x = pack_bf16x2(lt != 0.f ? t.x * inv : 0.f, lt != 0.f ? t.y * inv : 0.f);
+            pk.y = pack_bf16x2(lt != 0.f ? t.z * inv : 0.f, lt != 0.f ? t.w * inv : 0.f);
+            *reinterpret_cast<uint2 *>(out + (size_t)(row0 + r) * kL + 4 * ct) = pk;
+            if (lse && ct == 0)
+                lse[row0 + r] = lt != 0.f ? (Ma + log2f(lt)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();
+    }
+}
+
+// Workspace: partial O rows fp32 [2 x grid][64][512], (m, l) [2 x grid][64],
+// merge entries [grid]. It does not grow with the batch.
+constexpr size_t kPmPartBytes = (size_t)2 * kPmGrid * kPmRows * kL * sizeof(float);
+constexpr size_t kPmMlBytes = (size_t)2 * kPmGrid * kPmRows * sizeof(float2);
+inline size_t prefix_mla_workspace_bytes(int Q, int Hm) {
+    return Q > 0 && Hm > 0 ? kPmPartBytes + kPmMlBytes + kPmGrid * sizeof(MergeEntry) : 0;
+}
+
+template <bool kFp8, int kWidth>
+inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, int Hm,
+                          float scale_log2, float out_scale, void *out, float *lse, void *ws,
+                          cudaStream_t stream) {
+    CUtensorMap map = {};
+    int box_rows = 0;
+    if (!kFp8 && g.page % 16 == 0 && g.kv_rows >= kPmTile) {
+        box_rows = g.page % 32 == 0 ? 32 : 16;
+        if (!make_map_bf16_2d(&map, kv, (uint64_t)g.kv_rows, kWidth, kWidth * 2, 64, box_rows))
+            return DSA_ERR_CUDA;
+    }
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(prefix_mla_kernel<kFp8, kWidth>),
+                          PmSmem<kWidth>::kBytes))
+        return DSA_ERR_CUDA;
+    auto *part = reinterpret_cast<float *>(ws);
+    auto *ml = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(ws) + kPmPartBytes);
+    auto *merge = reinterpret_cast<MergeEntry *>(reinterpret_cast<uint8_t *>(ws) + kPmPartBytes + kPmMlBytes);
+    auto *ob = reinterpret_cast<__nv_bfloat16 *>(out);
+    if (launch_pdl(prefix_mla_kernel<kFp8, kWidth>, dim3(kPmGrid), dim3(kPmThreads),
+                   PmSmem<kWidth>::kBytes, stream, map, box_rows,
+                   reinterpret_cast<const __nv_bfloat16 *>(q), kv, g, Hm, scale_log2, out_scale, part,
+                   ml, merge, ob, lse) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    const int st = launch_status();
+    if (st != DSA_OK) return st;
+    // Few row tiles are split into many parts: an entry a tile and a block a row.
+    // Many are split at most where a CTA's range ends: an entry a CTA, 8 rows a block.
+    const RowTiles rt(g.Q, Hm);
+    const bool by_tile = rt.count <= kPmGrid;
+    const int rpb = by_tile ? 1 : 8;
+    if (launch_pdl(prefix_mla_merge_kernel, dim3(by_tile ? rt.count : kPmGrid, kPmRows / rpb),
+                   dim3(kMergeGroups * 128), 0, stream, part, ml, merge, g.Q, Hm, rpb, out_scale, ob,
+                   lse) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    return launch_status();
+}
 
 template <bool kFp8>
 inline int prefix_mla_launch(const void *q, const void *kv, float kv_scale, int64_t kv_rows,
@@ -126,12 +941,11 @@ inline int prefix_mla_launch(const void *q, const void *kv, float kv_scale, int6
     if (!ws || ws_bytes < prefix_mla_workspace_bytes(g.Q, Hm)) return DSA_ERR_WORKSPACE;
     g.kv_rows = (int)kv_rows;
     const float scale_log2 = (kFp8 ? sm_scale * kv_scale : sm_scale) * 1.4426950408889634f;
-    const long long blocks = ((long long)g.Q * Hm + 3) / 4;
-    if (launch_pdl(prefix_mla_plain_kernel<kFp8>, dim3((unsigned)blocks), dim3(128), 0, stream,
-                   reinterpret_cast<const __nv_bfloat16 *>(q), kv, g, Hm, rope, scale_log2,
-                   kFp8 ? kv_scale : 1.0f, reinterpret_cast<__nv_bfloat16 *>(out), lse) != cudaSuccess)
-        return DSA_ERR_CUDA;
-    return launch_status();
+    const float out_scale = kFp8 ? kv_scale : 1.0f;
+    return rope ? prefix_mla_run<kFp8, DSA_KV_LORA + kRopeDim>(q, kv, g, Hm, scale_log2, out_scale,
+                                                               out, lse, ws, stream)
+                : prefix_mla_run<kFp8, DSA_KV_LORA>(q, kv, g, Hm, scale_log2, out_scale, out, lse, ws,
+                                                    stream);
 }
 
 }  // namespace dsa
