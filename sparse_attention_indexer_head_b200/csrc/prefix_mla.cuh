@@ -59,7 +59,8 @@ constexpr int kPmTile = 32;                           // tokens of a unit: one S
 constexpr int kPmRows = 64;                           // (query, head) rows of a row tile
 constexpr int kPmGrid = 148;                          // persistent CTAs, one per SM
 constexpr int kPmMinUnits = 4;                        // units a CTA takes at least
-constexpr int kPmThreads = 512;
+constexpr int kPmThreads = 448;                       // 4 softmax warps, 8 loaders, S and PV issuers
+constexpr int kPmIssuer = 12;
 constexpr int kPmQueries = 4;                         // queries a row tile holds at most
 
 // How (query, head) rows are cut into row tiles: qpt queries of Hm < 64 heads
@@ -121,32 +122,34 @@ struct TileWalk {
 
 // What a ring slot holds, written by its loader for the issuers and the softmax.
 struct UnitInfo {
-    int tile;                                         // row tile
-    int row0, nrows;                                  // its rows that see these tokens
-    int active;                                       // its queries that see any token
+    int rows;                                         // first row | rows << 8 that see these tokens
+    int flags;                                        // kUnit* | queries that see any token << 8
     uint32_t valid;                                   // tokens of the unit that exist
-    int flags;                                        // kUnit*
     int part;                                         // partial slot, -1: the tile is whole
-    int pad;
 };
-enum : int { kUnitFirst = 1, kUnitLast = 2, kUnitFresh = 4 };   // of the part; rows not yet summed
+// First and last unit of the part; rows not yet summed; rows copied without TMA.
+enum : int { kUnitFirst = 1, kUnitLast = 2, kUnitFresh = 4, kUnitCopied = 8 };
 
 struct MergeEntry { int tile, first_cta, parts, pad; };
 
-constexpr int kPmSlots = 4;                           // ring slots of one unit
-constexpr int kPmSBufs = 4;                           // S buffers in tensor memory
+constexpr int kPmSBufs = 2;                           // S buffers in tensor memory
 constexpr uint32_t kPmSCol = 256;                     // behind O^T
-constexpr uint32_t kPmAtom = kPmSlots * kPmTile * 128;   // 64 channels of the whole ring
-constexpr uint32_t kPmSlotRows = kPmTile * 128;       // a slot's rows within an atom
+// Tensor memory's other columns hold the queries' first 384 channels: S reads
+// them there instead of 2 KB of shared memory a K-step, and shared memory's
+// 128 bytes a cycle are what bounds S, PV and the copies together.
+constexpr int kPmQSteps = 24;                         // K-steps of 16 channels, 8 columns each
+constexpr uint32_t kPmQCol = kPmSCol + kPmSBufs * kPmTile;
+constexpr int kPmQChannels = kPmQSteps * 16;
+constexpr uint32_t kPmAtom = kPmTile * 128;           // 64 channels of a slot's rows
 constexpr uint32_t kPmPBytes = kPmRows * 128;         // two P buffers, the halves of 128-byte rows
-static_assert(kPmSCol + kPmSBufs * kPmTile <= 512, "tensor memory columns");
+static_assert(kPmQCol + kPmQSteps * 8 <= 512, "tensor memory columns");
+constexpr int kPmMaxSlots = 6;
 
 struct PmCtl {
-    uint64_t kv_full[kPmSlots], kv_empty[kPmSlots];
+    uint64_t kv_full[kPmMaxSlots], kv_empty[kPmMaxSlots];
     uint64_t s_full[kPmSBufs], s_empty[kPmSBufs];
-    uint64_t p_full[2], p_empty[2];
-    uint64_t o_done, o_final, q_full, fin;
-    UnitInfo unit[kPmSlots];
+    uint64_t p_full[2], q_full, fin;
+    UnitInfo unit[kPmMaxSlots];
     float alpha[kPmRows], linv[kPmRows];
     long long warp_sum[16];
     long long total, per, begin;
@@ -158,13 +161,17 @@ struct PmCtl {
 template <int kWidth>
 struct PmSmem {
     static constexpr int kAtoms = kWidth / 64;
-    static constexpr uint32_t kQ = 0;                               // kAtoms x [64 rows x 128 B]
-    static constexpr uint32_t kKV = kAtoms * kPmRows * 128;         // kAtoms x [128 rows x 128 B]
-    static constexpr uint32_t kP = kKV + kAtoms * kPmAtom;
+    static constexpr int kQAtoms = kAtoms - kPmQChannels / 64;      // of the queries, the others in tensor memory
+    static constexpr int kSlots = kWidth > DSA_KV_LORA ? 5 : 6;     // ring slots of one unit, as many as fit
+    static constexpr uint32_t kQ = 0;                               // kQAtoms x [64 rows x 128 B]
+    static constexpr uint32_t kKV = kQAtoms * kPmRows * 128;        // slots x kAtoms x [32 rows x 128 B]
+    static constexpr uint32_t kSlot = kAtoms * kPmAtom;
+    static constexpr uint32_t kP = kKV + kSlots * kSlot;
     static constexpr uint32_t kCtl = kP + kPmPBytes;
     static constexpr int kBytes = (int)kCtl + (int)sizeof(PmCtl) + 1024;   // + alignment slack
 };
-static_assert(PmSmem<576>::kBytes <= 232448, "shared memory per block");
+static_assert(PmSmem<576>::kBytes <= 232448 && PmSmem<512>::kBytes <= 232448, "shared memory per block");
+static_assert(PmSmem<576>::kSlots <= kPmMaxSlots && PmSmem<512>::kSlots <= kPmMaxSlots, "ring");
 static_assert(65535 * 2 <= (int)(kPmPBytes / 8) * kPmThreads, "block sums hold every row tile");
 
 DSA_DEVINL bool pm_wait(PmCtl *ctl, uint64_t *bar, uint32_t parity) {
@@ -267,7 +274,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                   MergeEntry *__restrict__ merge, __nv_bfloat16 *__restrict__ out,
                   float *__restrict__ lse) {
     using S = PmSmem<kWidth>;
-    constexpr int kAtoms = S::kAtoms;
+    constexpr int kAtoms = S::kAtoms, kPmSlots = S::kSlots;
     extern __shared__ uint8_t pm_smem_raw[];
     const uint32_t raw = smem_u32(pm_smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;           // 128B-swizzle atoms need 1 KB
@@ -278,11 +285,11 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const RowTiles rt(g.Q, Hm);
 
-    if (warp == 0) {
+    if (warp == kPmIssuer) {
         tc::tmem_alloc(&ctl->tmem_base, 512);
         tc::tmem_relinquish();
     }
-    if (tid == 32) {
+    if (tid == 0) {
         for (int i = 0; i < kPmSlots; ++i) {
             mbar_init(&ctl->kv_full[i], 4 * 32 + 4);  // four warps' lanes' copies + a word from each warp
             mbar_init(&ctl->kv_empty[i], 1);
@@ -293,10 +300,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->p_full[i], 128);
-            mbar_init(&ctl->p_empty[i], 1);
         }
-        mbar_init(&ctl->o_done, 1);
-        mbar_init(&ctl->o_final, 1);
         mbar_init(&ctl->q_full, 128);
         mbar_init(&ctl->fin, 2);
         ctl->abort = 0;
@@ -324,77 +328,90 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         merge[blockIdx.x] = e;
     }
 
-    if (warp == 0) {
+    if (warp == kPmIssuer) {
         // ------------------------------------------------------------------ S issuer
-        // S(c)[64 rows x 32 tokens] = Q K^T, kWidth / 16 K-steps.
+        // S(c)[64 rows x 32 tokens] = Q K^T, kWidth / 16 K-steps. Two S buffers let it
+        // run up to two units ahead of PV. The waits are blocking and in a fixed order,
+        // in a warp of its own: with the pipe reading operands, one access to shared
+        // memory takes over 100 cycles, and a loop that polls for either product
+        // spent 600 cycles a turn.
         constexpr uint32_t idS = tc::idesc_bf16(64, kPmTile, false, false);
+        const uint64_t a0 = tc::desc_sw128(sQ, 16, 1024);
         bool ok = true;
-        int parts = 0;
-        for (int c = 0; ok && c < n; ++c) {
-            const int slot = c % kPmSlots, sb = c % kPmSBufs;
+        int parts = 0, slot = 0;
+        for (int c = 0; c < n; ++c) {
+            const int sb = c % kPmSBufs;
             ok = pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
-            if (ok && (ctl->unit[slot].flags & kUnitFirst)) ok = pm_wait(ctl, &ctl->q_full, parts++ & 1);
+            const int flags = ctl->unit[slot].flags;
             if (ok && c >= kPmSBufs) ok = pm_wait(ctl, &ctl->s_empty[sb], ((c / kPmSBufs) - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if (ok && (flags & kUnitFirst)) ok = pm_wait(ctl, &ctl->q_full, parts++ & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after_sync();
-            tc::fence_proxy_async_smem();                 // the slot may have been written by cp.async
+            if (flags & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
             if (elect_one()) {
                 const uint32_t d = tmem + kPmSCol + (uint32_t)(sb * kPmTile);
-                const uint64_t a0 = tc::desc_sw128(sQ, 16, 1024);
-                const uint64_t b0 = tc::desc_sw128(sKV + slot * kPmSlotRows, 16, 1024);
+                const uint64_t b0 = tc::desc_sw128(sKV + slot * S::kSlot, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < kWidth / 16; ++kk)
-                    tc::mma_bf16_ss(d, a0 + (uint64_t)(((kk >> 2) * kPmRows * 128 + (kk & 3) * 32) >> 4),
+                for (int kk = 0; kk < kPmQSteps; ++kk)
+                    tc::mma_bf16_ts(d, tmem + kPmQCol + kk * 8,
                                     b0 + (uint64_t)(((kk >> 2) * kPmAtom + (kk & 3) * 32) >> 4), idS,
                                     kk > 0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = kPmQSteps; kk < kWidth / 16; ++kk) {
+                    const int ka = kk - kPmQSteps;
+                    tc::mma_bf16_ss(d, a0 + (uint64_t)(((ka >> 2) * kPmRows * 128 + (ka & 3) * 32) >> 4),
+                                    b0 + (uint64_t)(((kk >> 2) * kPmAtom + (kk & 3) * 32) >> 4), idS, 1u);
+                }
                 tc::mma_commit(&ctl->s_full[sb]);
             }
             __syncwarp();
+            if (++slot == kPmSlots) slot = 0;
         }
+        __syncwarp();
         if (elect_one()) tc::mma_commit(&ctl->fin);
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == kPmIssuer + 1) {
         // ------------------------------------------------------------------ PV issuer
-        // O^T[128 b .. + 127][the unit's rows] += V^T P^T for the four 128-channel
-        // blocks b: rows are the N dimension, so a unit that one query sees touches
-        // that query's columns alone (a NaN among its values reaches no other).
+        // PV(c): O^T[128 b .. + 127][the unit's rows] += V^T P^T for the four
+        // 128-channel blocks b. Rows are the N dimension of PV, so a unit that one
+        // query sees touches that query's columns alone (a NaN among its values
+        // reaches no other).
         bool ok = true;
-        for (int c = 0; ok && c < n; ++c) {
-            const int slot = c % kPmSlots, pb = c & 1;
-            ok = pm_wait(ctl, &ctl->p_full[pb], (c >> 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+        int slot = 0;
+        for (int c = 0; c < n; ++c) {
+            const int pb = c & 1;
+            ok = pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
+            const uint32_t rows = (uint32_t)__shfl_sync(0xffffffffu, ctl->unit[slot].rows, 0);
+            const uint32_t flags = (uint32_t)__shfl_sync(0xffffffffu, ctl->unit[slot].flags, 0);
+            const uint32_t row0 = rows & 255u;
+            if (ok) ok = pm_wait(ctl, &ctl->p_full[pb], (c >> 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after_sync();
-            tc::fence_proxy_async_smem();                 // the slot may have been written by cp.async
-            const int row0 = __shfl_sync(0xffffffffu, ctl->unit[slot].row0, 0);
-            const int nrows = __shfl_sync(0xffffffffu, ctl->unit[slot].nrows, 0);
-            const int flags = __shfl_sync(0xffffffffu, ctl->unit[slot].flags, 0);
+            if (flags & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
             if (elect_one()) {
-                const uint32_t id = (tc::idesc_bf16(128, 0, true, false)) | ((uint32_t)(nrows >> 3) << 17);
+                const uint32_t id = tc::idesc_bf16(128, 0, true, false) | ((rows >> 8) >> 3 << 17);
                 // V^T: MN-major, 64-channel atoms kPmAtom apart, 8-token groups 1 KB apart
-                const uint64_t a0 = tc::desc_sw128(sKV + slot * kPmSlotRows, kPmAtom, 1024);
+                const uint64_t a0 = tc::desc_sw128(sKV + slot * S::kSlot, kPmAtom, 1024);
                 // P^T: K-major, 128-byte rows (this buffer's half), 8-row groups 1 KB apart
                 const uint64_t b0 = tc::desc_sw128(sP + row0 * 128 + pb * 64, 16, 1024);
 #pragma unroll
                 for (int ks = 0; ks < kPmTile / 16; ++ks)
 #pragma unroll
                     for (int blk = 0; blk < 4; ++blk)
-                        tc::mma_bf16_ss(tmem + (uint32_t)(blk * kPmRows + row0),
+                        tc::mma_bf16_ss(tmem + (uint32_t)(blk * kPmRows) + row0,
                                         a0 + (uint64_t)((blk * 2 * kPmAtom + ks * 2048) >> 4),
                                         b0 + (uint64_t)((ks * 32) >> 4), id,
                                         (ks > 0 || !(flags & kUnitFresh)) ? 1u : 0u);
                 tc::mma_commit(&ctl->kv_empty[slot]);
-                tc::mma_commit(&ctl->p_empty[pb]);
-                tc::mma_commit(&ctl->o_done);
-                if (flags & kUnitLast) tc::mma_commit(&ctl->o_final);
             }
             __syncwarp();
+            if (++slot == kPmSlots) slot = 0;
         }
+        __syncwarp();
         if (elect_one()) tc::mma_commit(&ctl->fin);
         __syncwarp();
-    } else if (warp >= 8) {
-        // ------------------------------------------------------------------ loaders
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------------ loaders (warps 4-11)
         // Two groups of four warps fill alternate units. Lane l of every warp finds
         // the cache row of the unit's token l. Where the 32 rows are whole boxes of
         // the tensor map (pages that are a multiple of 16 rows, away from the ends
@@ -402,7 +419,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         // copies rows 8i .. 8i+7 in 16-byte pieces, zero-filled where there is no
         // token: what lies behind a sequence may hold anything, and a weight of 0
         // times a NaN would not be 0.
-        const int grp = (warp - 8) >> 2, sub = (warp - 8) & 3;
+        const int grp = (warp - 4) >> 2, sub = (warp - 4) & 3;
         TileWalk w;
         int tile = n > 0 ? ctl->first_tile : 0, u = n > 0 ? ctl->first_unit : 0;
         int part_begin = u;                               // the part's first unit in its tile
@@ -436,17 +453,13 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             const int part_last = min(w.units, u + left) - 1;
             const bool none = w.active == 0;              // no query sees a token: an empty unit
             if (none) { rows0 = 0; rowsn = kPmRows; }
-            info.tile = tile;
-            info.row0 = rows0;
-            info.nrows = rowsn;
-            info.active = w.active;
+            info.rows = rows0 | (rowsn << 8);
             const bool pre_seen = w.shared && part_begin < w.npre;
             const bool fresh = u == part_begin || (k >= 0 && seg_unit == 0 && !pre_seen);
             info.flags = (u == part_begin ? kUnitFirst : 0) | (u == part_last ? kUnitLast : 0) |
-                         (fresh ? kUnitFresh : 0);
+                         (fresh ? kUnitFresh : 0) | (w.active << 8);
             const bool whole = part_begin == 0 && part_last == w.units - 1;
             info.part = whole ? -1 : 2 * (int)blockIdx.x + (part_begin == 0 ? 1 : 0);
-            info.pad = 0;
             const int t = tok0 + lane;
             int row = -1;
             if (!none && t >= s0 && t < s1) row = g.row(b, t, P);
@@ -473,14 +486,12 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
 
         bool more = n > 0;
         if (grp == 1) more = more && advance();
-        UnitInfo info, next_info;
-        int row = -1, next_row = -1;
+        UnitInfo info;
+        int row = -1;
         if (more) row = describe(info);
         for (int c = grp; more; c += 2) {
             const int slot = c % kPmSlots;
-            const bool next = advance() && advance();
-            if (next) next_row = describe(next_info);     // its page lookups run behind this unit's copies
-            const uint32_t dst0 = sKV + slot * kPmSlotRows;
+            const uint32_t dst0 = sKV + slot * S::kSlot;
             bool ok = true;
             if constexpr (!kFp8) {
                 if (c >= kPmSlots) ok = pm_wait(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
@@ -492,15 +503,20 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 }
                 if (boxes) {
                     const int row_b = __shfl_sync(0xffffffffu, row, box_rows & 31);   // the second box
+                    const int row_a = __shfl_sync(0xffffffffu, row, 0);
                     if (sub == 0) {
-                        if (lane == 0) {
+                        if (elect_one()) {
                             ctl->unit[slot] = info;
                             mbar_arrive_expect_tx(&ctl->kv_full[slot], kPmTile * kWidth * 2);
-                            for (int a = 0; a < kAtoms; ++a) {
-                                tma_load_2d(dst0 + a * kPmAtom, &kv_map, a * 64, row, &ctl->kv_full[slot]);
-                                if (box_rows == 16)
-                                    tma_load_2d(dst0 + a * kPmAtom + 16 * 128, &kv_map, a * 64, row_b,
+                            if (box_rows == kPmTile) {
+                                tma_load_3d(dst0, &kv_map, 0, row_a, 0, &ctl->kv_full[slot]);
+                            } else {
+#pragma unroll
+                                for (int a = 0; a < kAtoms; ++a) {
+                                    tma_load_3d(dst0 + a * kPmAtom, &kv_map, 0, row_a, a, &ctl->kv_full[slot]);
+                                    tma_load_3d(dst0 + a * kPmAtom + 16 * 128, &kv_map, 0, row_b, a,
                                                 &ctl->kv_full[slot]);
+                                }
                             }
                         }
                     } else if (lane == 0) {
@@ -536,6 +552,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                         }
                     }
                     if (lane == 0) {
+                        info.flags |= kUnitCopied;
                         if (sub == 0) ctl->unit[slot] = info;
                         mbar_arrive(&ctl->kv_full[slot]);
                     }
@@ -583,88 +600,144 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 }
                 mbar_arrive(&ctl->kv_full[slot]);
             }
-            more = next;
-            info = next_info;
-            row = next_row;
+            more = advance() && advance();
+            if (more) row = describe(info);               // its page lookups run behind this unit's copies
         }
         tc::cp_async_wait_all();          // nothing of this warp in flight past here
-    } else if (warp >= 4) {
-        // ------------------------------------------------------------------ softmax (warps 4-7)
-        // S is read with the 16x64b tensor-memory shape: thread t of warp 4+wq holds
+    } else {
+        // ------------------------------------------------------------------ softmax (warps 0-3)
+        // S is read with the 16x64b tensor-memory shape: thread t of warp wq holds
         // row hh = 16 wq + (t>>2) + 8 (t&1) and the unit's tokens of parity
         // par = (t>>1)&1; its partner t^2 holds the other parity of the same row.
-        const int wq = warp - 4, wtid = tid - 128;
+        const int wq = warp, wtid = tid;
         const int hh = 16 * wq + (lane >> 2) + 8 * (lane & 1);
         const int par = (lane >> 1) & 1;
         const bool owner = par == 0;          // writes the row's values
         const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
         const int hq = rt.qpt > 1 ? hh / Hm : 0;   // the row's query within its tile
         float m_used = -INFINITY, l = 0.f;
-        int parts = 0;
         bool failed = false;
 
-        // Q rows of a row tile into the swizzled K-major layout
+        // The queries of a row tile: channels from 384 on into shared memory (swizzled,
+        // K-major), the others into tensor memory, where this thread's row hh has its
+        // pairs of channels as columns: thread and partner load alternate 16-byte
+        // vectors (four columns) and swap the columns of the other's parity.
         auto load_q = [&](int tile) {
             const int row0 = rt.first_row(tile), nr = rt.rows(tile);
-            constexpr int kPieces = kWidth / 8;
+            constexpr int kPieces = S::kQAtoms * 8;
             for (int x = wtid; x < kPmRows * kPieces; x += 128) {
                 const int r = x / kPieces, cc = x % kPieces;
                 const uint32_t dst = sQ + (cc >> 3) * (kPmRows * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
                 if (r < nr)
-                    tc::cp_async16(dst, q + (size_t)(row0 + r) * kWidth + cc * 8);
+                    tc::cp_async16(dst, q + (size_t)(row0 + r) * kWidth + kPmQChannels + cc * 8);
                 else
                     tc::st_shared_zero16(dst);
             }
+            const uint4 *src = reinterpret_cast<const uint4 *>(q + (size_t)(row0 + min(hh, nr - 1)) * kWidth) + par;
+            constexpr int kBatch = kPmQSteps * 8 / 32 / 2;    // 32-column blocks in flight
+#pragma unroll
+            for (int b0 = 0; b0 < 2; ++b0) {
+                uint4 v[kBatch][4];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[b][i] = src[(b0 * kBatch + b) * 8 + 2 * i];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // columns 8i + 4 par .. + 3 of the block are here; keep those of parity par
+                        const uint32_t s0 = par ? v[b][i].x : v[b][i].y, s1 = par ? v[b][i].z : v[b][i].w;
+                        const uint32_t k0 = par ? v[b][i].y : v[b][i].x, k1 = par ? v[b][i].w : v[b][i].z;
+                        const uint32_t g0 = __shfl_xor_sync(0xffffffffu, s0, 2);
+                        const uint32_t g1 = __shfl_xor_sync(0xffffffffu, s1, 2);
+                        // register j is column par + 2j
+                        o[4 * i + 0] = par ? g0 : k0;
+                        o[4 * i + 1] = par ? g1 : k1;
+                        o[4 * i + 2] = par ? k0 : g0;
+                        o[4 * i + 3] = par ? k1 : g1;
+                    }
+                    if (hh >= nr)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = 0u;
+                    tc::tmem_st16x64b_x16(tl + kPmQCol + (uint32_t)((b0 * kBatch + b) * 32), o);
+                }
+            }
+            tc::tmem_wait_st();
         };
         auto release_q = [&]() {
             tc::cp_async_wait_all();
             tc::fence_proxy_async_smem();
+            tc::fence_before_sync();
             mbar_arrive(&ctl->q_full);
         };
-        int next_tile = n > 0 ? ctl->first_tile : 0;
+        int tile = n > 0 ? ctl->first_tile : 0;       // a CTA's parts are consecutive row tiles
         if (n > 0) {
-            load_q(next_tile++);
+            load_q(tile);
             release_q();
         }
+        // Ring positions and parities of units c, c - 1 and c - 2 (a PV frees its slot,
+        // and has then read its P buffer).
+        int slot = 0, slot1 = 0, slot2 = 0;
+        uint32_t par0 = 0, par1 = 0, par2 = 0;
+        UnitInfo info = {};
+        if (n > 0) {
+            (void)pm_wait(ctl, &ctl->kv_full[0], 0);
+            info = ctl->unit[0];
+        }
         for (int c = 0; c < n; ++c) {
-            const int slot = c % kPmSlots, pb = c & 1, sb = c % kPmSBufs;
-            bool bad = !pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
-            const UnitInfo info = ctl->unit[slot];
-            bad = bad || !pm_wait(ctl, &ctl->s_full[sb], (c / kPmSBufs) & 1);
+            const int pb = c & 1, sb = c % kPmSBufs;
+            const int nslot = slot + 1 == kPmSlots ? 0 : slot + 1;
+            const uint32_t npar = nslot == 0 ? par0 ^ 1u : par0;
+            bool bad = !pm_wait(ctl, &ctl->s_full[sb], (c / kPmSBufs) & 1);
             tc::fence_after_sync();
             uint32_t sr[16];                              // tokens par + 2i
             tc::tmem_ld16x64b_x16(tl + kPmSCol + (uint32_t)(sb * kPmTile), sr);
+            // What the end of this turn needs, asked for while the scores arrive: shared
+            // memory answers slowly while the tensor cores read their operands.
+            const bool next_ready = c + 1 < n && mbar_test(&ctl->kv_full[nslot], npar);
+            const bool p_free = c < 2 || mbar_test(&ctl->kv_empty[slot2], par2);
             tc::tmem_wait_ld();
             tc::fence_before_sync();
             mbar_arrive(&ctl->s_empty[sb]);
+            UnitInfo next = info;
+            if (next_ready) next = ctl->unit[nslot];
 
-            const bool mine = hh >= info.row0 && hh < info.row0 + info.nrows &&
-                              ((info.active >> hq) & 1);
+            const int urow0 = info.rows & 255;
+            const bool mine = hh >= urow0 && hh < urow0 + (info.rows >> 8) && ((info.flags >> (8 + hq)) & 1);
             const uint32_t vm = mine ? info.valid >> par : 0u;
             float z[16];
-            float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                z[i] = ((vm >> (2 * i)) & 1) ? __uint_as_float(sr[i]) * scale_log2 : -INFINITY;
-                mx = fmaxf(mx, z[i]);
+            for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(sr[i]) * scale_log2;
+            if ((vm & 0x55555555u) != 0x55555555u) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[i] = ((vm >> (2 * i)) & 1) ? z[i] : -INFINITY;
             }
+            float m4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(z[i], z[i + 4]), fmaxf(z[i + 8], z[i + 12]));
+            float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             float alpha = 1.f;
             bool moved = false;
             if (mx > m_used + kLazyRescale) {
-                moved = m_used != -INFINITY;          // nothing summed before: nothing to rescale
+                // nothing summed before: nothing to rescale
+                moved = m_used != -INFINITY && !(info.flags & kUnitFirst);
                 alpha = ex2(m_used - mx);
                 m_used = mx;
             }
-            float psum = 0.f;
+            // a row without a token so far: its weights are 0 (z = -inf) and not NaN
+            const float m_ref = m_used == -INFINITY ? 0.f : m_used;
+            float p4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                z[i] = z[i] == -INFINITY ? 0.f : ex2(z[i] - m_used);
-                psum += z[i];        // fp32 weights: the row sum and lse stay exact to fp32
+                z[i] = ex2(z[i] - m_ref);
+                p4[i & 3] += z[i];   // fp32 weights: the row sum and lse stay exact to fp32
             }
+            float psum = (p4[0] + p4[1]) + (p4[2] + p4[3]);
             psum += __shfl_xor_sync(0xffffffffu, psum, 2);
             l = fmaf(l, alpha, psum);
-            if (owner) ctl->alpha[hh] = alpha;
             // bf16 P row: this thread packs tokens 16 par .. 16 par + 15, taking the
             // other parity from its partner.
             uint32_t pk[8];
@@ -673,13 +746,12 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 const float recv = __shfl_xor_sync(0xffffffffu, par ? z[k] : z[k + 8], 2);
                 pk[k] = par ? pack_bf16x2(recv, z[k + 8]) : pack_bf16x2(z[k], recv);
             }
-            bad = bad || (c >= 2 && !pm_wait(ctl, &ctl->p_empty[pb], ((c >> 1) - 1) & 1));
+            if (!p_free) bad = bad || !pm_wait(ctl, &ctl->kv_empty[slot2], par2);
             // One barrier a unit; a second only when some row rescales or a wait failed.
-            const bool first = (info.flags & kUnitFirst) != 0;
-            bool need = false;
-            if (tc::named_bar_or(2, 128, bad || (!first && moved))) {
+            const bool need = tc::named_bar_or(2, 128, bad || moved);
+            if (need) {
+                if (owner) ctl->alpha[hh] = alpha;
                 if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
-                need = true;
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -691,7 +763,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             }
             if (need) {
                 // O^T columns of rescaled rows times alpha, after PV(c-1) has landed
-                bad = !pm_wait(ctl, &ctl->o_done, (c - 1) & 1);
+                bad = !pm_wait(ctl, &ctl->kv_empty[slot1], par1);
                 if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
                 tc::fence_after_sync();
 #pragma unroll 1
@@ -707,24 +779,39 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
+                tc::named_bar_sync(2, 128);       // alpha is read before the next unit writes it
             }
             tc::fence_proxy_async_smem();
             mbar_arrive(&ctl->p_full[pb]);
-            if (!(info.flags & kUnitLast)) continue;
+            const UnitInfo cur = info;
+            const int cslot = slot;
+            const uint32_t cpar = par0;
+            if (c + 1 < n) {
+                if (!next_ready) {
+                    (void)pm_wait(ctl, &ctl->kv_full[nslot], npar);
+                    next = ctl->unit[nslot];
+                }
+                info = next;
+            }
+            slot2 = slot1; par2 = par1;
+            slot1 = slot; par1 = par0;
+            slot = nslot; par0 = npar;
+            if (!(cur.flags & kUnitLast)) continue;
 
             // -------------------------------------------------------------- end of a part
             // Every S of this part is done: the next row tile's queries are loaded while
             // the last PV runs, and its products start behind this part's output.
             const bool more = c + 1 < n;
-            if (more) load_q(next_tile++);
-            bad = !pm_wait(ctl, &ctl->o_final, parts++ & 1);
+            if (more) load_q(tile + 1);
+            bad = !pm_wait(ctl, &ctl->kv_empty[cslot], cpar);   // the part's last PV
             if (owner) ctl->linv[hh] = l != 0.f ? out_scale / l : 0.f;
             if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
             if (more) release_q();
             tc::fence_after_sync();
-            const int nr = rt.rows(info.tile);
-            const size_t row0 = (size_t)rt.first_row(info.tile);
-            if (info.part < 0) {
+            const int nr = rt.rows(tile);
+            const size_t row0 = (size_t)rt.first_row(tile);
+            ++tile;
+            if (cur.part < 0) {
                 if (lse && owner && hh < nr)
                     lse[row0 + hh] = l != 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
                 // Lanes 2i and 2i+1 hold channels L, L+1: the even lane writes both
@@ -750,8 +837,8 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                     }
                 }
             } else {
-                if (owner) part_ml[(size_t)info.part * kPmRows + hh] = make_float2(m_used, l);
-                float *po = part + (size_t)info.part * kPmRows * kL;
+                if (owner) part_ml[(size_t)cur.part * kPmRows + hh] = make_float2(m_used, l);
+                float *po = part + (size_t)cur.part * kPmRows * kL;
 #pragma unroll 1
                 for (int blk = 0; blk < 8; ++blk) {
                     uint32_t o[32];
@@ -776,11 +863,11 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
 
     // Every MMA of this CTA has completed before tensor memory is released.
     __syncwarp();
-    if (warp == 0) (void)mbar_wait(&ctl->fin, 0);
+    if (warp == kPmIssuer) (void)mbar_wait(&ctl->fin, 0);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    if (warp == kPmIssuer) tc::tmem_dealloc(tmem, 512);
 }
 
 // Row tiles that were split: entry blockIdx.x, kRowsPerBlock rows a block. 512
@@ -885,7 +972,9 @@ inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, in
     int box_rows = 0;
     if (!kFp8 && g.page % 16 == 0 && g.kv_rows >= kPmTile) {
         box_rows = g.page % 32 == 0 ? 32 : 16;
-        if (!make_map_bf16_2d(&map, kv, (uint64_t)g.kv_rows, kWidth, kWidth * 2, 64, box_rows))
+        // whole pages of 32 rows: a unit is one box of all its 64-channel atoms
+        if (!make_map_bf16_atoms(&map, kv, (uint64_t)g.kv_rows, kWidth / 64, box_rows,
+                                 box_rows == kPmTile ? kWidth / 64 : 1))
             return DSA_ERR_CUDA;
     }
     if (!ensure_smem_attr(reinterpret_cast<const void *>(prefix_mla_kernel<kFp8, kWidth>),
