@@ -106,10 +106,20 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_raw_stream = None          # device index -> its current stream's handle, once CUDA is up
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            torch.cuda.current_stream()         # brings CUDA up
+            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        get, device = _raw_stream               # 0.2 us; the stream object takes 4
+        return get(device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

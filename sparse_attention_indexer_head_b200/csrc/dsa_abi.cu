@@ -275,7 +275,7 @@ int dsa_prefix_mla_decode_paged(const dsa_bf16 *q, const dsa_bf16 *kv, int64_t k
                                 float *lse, void *workspace, size_t workspace_bytes,
                                 dsa_stream_t stream) {
     const dsa::PrefixGeom g{prefix_table, prefix_len, block_table, seq_len, q_req, q_pos,
-                            prefix_blocks, max_blocks, page_size, Q, B, 0};
+                            prefix_blocks, max_blocks, page_size, Q, B, 0, 0};
     return dsa::prefix_mla_launch<false>(q, kv, 1.0f, kv_rows, g, Hm, kv_lora, rope_dim, sm_scale,
                                          out, lse, workspace, workspace_bytes,
                                          reinterpret_cast<cudaStream_t>(stream));
@@ -290,7 +290,7 @@ int dsa_prefix_mla_decode_paged_fp8(const dsa_bf16 *q, const uint8_t *kv8, float
                                     int rope_dim, float sm_scale, dsa_bf16 *out, float *lse,
                                     void *workspace, size_t workspace_bytes, dsa_stream_t stream) {
     const dsa::PrefixGeom g{prefix_table, prefix_len, block_table, seq_len, q_req, q_pos,
-                            prefix_blocks, max_blocks, page_size, Q, B, 0};
+                            prefix_blocks, max_blocks, page_size, Q, B, 0, 0};
     return dsa::prefix_mla_launch<true>(q, kv8, kv_scale, kv_rows, g, Hm, kv_lora, rope_dim,
                                         sm_scale, out, lse, workspace, workspace_bytes,
                                         reinterpret_cast<cudaStream_t>(stream));

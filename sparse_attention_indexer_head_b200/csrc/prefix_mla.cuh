@@ -21,6 +21,7 @@ struct PrefixGeom {
     const int32_t *seq_len, *q_req, *q_pos;
     int prefix_blocks, max_blocks, page, Q, B;
     int kv_rows;
+    int page_shift;                   // log2(page), -1 where page is no power of two
 
     // Tokens of the prefix that its pages can hold.
     DSA_DEVINL int shared_len() const {
@@ -28,27 +29,20 @@ struct PrefixGeom {
         const long long cap = (long long)prefix_blocks * page;
         return (int)max(0ll, min((long long)prefix_len[0], min(cap, (long long)kMaxTokens)));
     }
-    // Tokens 0 .. n-1 that query q sees; no more than its pages can hold.
-    DSA_DEVINL int visible(int q, int P) const {
-        const int b = q_req[q];
-        if (b < 0 || b >= B) return 0;
-        const long long n = min((long long)q_pos[q] + 1, (long long)seq_len[b]);
+    // Tokens 0 .. n-1 that a query at position pos of a sequence of len tokens sees; no
+    // more than its pages can hold.
+    DSA_DEVINL int visible(int pos, int len, int P) const {
+        const long long n = min((long long)pos + 1, (long long)len);
         const long long cap = max((long long)P, min((long long)max_blocks * page, (long long)kMaxTokens));
         return (int)max(0ll, min(n, cap));
     }
-    // Cache row of token t of request b, -1 where there is none.
-    DSA_DEVINL int row(int b, int t, int P) const {
-        const int bi = t / page;
-        int blk;
-        if (t < P) {
-            blk = __ldg(prefix_table + bi);
-        } else {
-            if (bi >= max_blocks) return -1;
-            blk = __ldg(block_table + (size_t)b * max_blocks + bi);
-        }
-        if (blk < 0) return -1;
+    // Cache row of token t of the request whose pages are `pages`, -1 where there is none.
+    DSA_DEVINL int row(const int32_t *pages, int t, int P) const {
+        const int bi = page_shift >= 0 ? t >> page_shift : t / page;
+        if (t >= P && bi >= max_blocks) return -1;
+        const int blk = __ldg((t < P ? prefix_table : pages) + bi);
         const long long r = (long long)blk * page + (t - bi * page);
-        return r < (long long)kv_rows ? (int)r : -1;
+        return blk >= 0 && r < (long long)kv_rows ? (int)r : -1;
     }
 };
 
@@ -59,7 +53,8 @@ constexpr int kPmTile = 32;                           // tokens of a unit: one S
 constexpr int kPmRows = 64;                           // (query, head) rows of a row tile
 constexpr int kPmGrid = 148;                          // persistent CTAs, one per SM
 constexpr int kPmMinUnits = 4;                        // units a CTA takes at least
-constexpr int kPmThreads = 448;                       // 4 softmax warps, 8 loaders, S and PV issuers
+constexpr int kPmPartUnits = 5;                       // units that a further part of a CTA costs
+constexpr int kPmThreads = 512;                       // 4 softmax warps, 8 loaders, S and PV issuers, 2 fetchers
 constexpr int kPmIssuer = 12;
 constexpr int kPmQueries = 4;                         // queries a row tile holds at most
 
@@ -91,27 +86,33 @@ struct TileWalk {
     int vis[kPmQueries], req[kPmQueries];
 
     DSA_DEVINL int query_units(int k, int P) const {
-        if (!shared) return (int)(((long long)vis[k] + kPmTile - 1) / kPmTile);
-        return vis[k] > P ? (int)(((long long)vis[k] + kPmTile - 1) / kPmTile) - P / kPmTile : 0;
+        const int end = (int)(((unsigned)vis[k] + kPmTile - 1) / kPmTile);
+        return !shared ? end : vis[k] > P ? end - (int)((unsigned)P / kPmTile) : 0;
     }
     DSA_DEVINL void load(const PrefixGeom &g, const RowTiles &rt, int t, int P) {
         const int q0 = rt.first_query(t);
         nq = min(rt.qpt, g.Q - q0);
         shared = rt.qpt > 1 && P > 0;
         active = 0;
+        int pos[kPmQueries], len[kPmQueries];
 #pragma unroll
         for (int k = 0; k < kPmQueries; ++k) {
-            vis[k] = 0;
-            req[k] = 0;
-            if (k < nq) {
-                vis[k] = g.visible(q0 + k, P);
-                req[k] = g.q_req[q0 + k];
-                active |= (vis[k] > 0 ? 1 : 0) << k;
-                shared = shared && (vis[k] == 0 || vis[k] >= P);
-            }
+            req[k] = k < nq ? g.q_req[q0 + k] : -1;
+            pos[k] = k < nq ? g.q_pos[q0 + k] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kPmQueries; ++k) {
+            const bool in = req[k] >= 0 && req[k] < g.B;
+            len[k] = in ? g.seq_len[req[k]] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kPmQueries; ++k) {
+            vis[k] = g.visible(pos[k], len[k], P);
+            active |= (vis[k] > 0 ? 1 : 0) << k;
+            shared = shared && (vis[k] == 0 || vis[k] >= P);
         }
         shared = shared && active != 0;
-        npre = shared ? (int)(((long long)P + kPmTile - 1) / kPmTile) : 0;
+        npre = shared ? (int)(((unsigned)P + kPmTile - 1) / kPmTile) : 0;
         units = npre;
 #pragma unroll
         for (int k = 0; k < kPmQueries; ++k)
@@ -122,13 +123,18 @@ struct TileWalk {
 
 // What a ring slot holds, written by its loader for the issuers and the softmax.
 struct UnitInfo {
-    int rows;                                         // first row | rows << 8 that see these tokens
-    int flags;                                        // kUnit* | queries that see any token << 8
+    // first row | rows << 8 that see these tokens | kUnit* << 16 | queries that see any token << 24
+    uint32_t word;
     uint32_t valid;                                   // tokens of the unit that exist
     int part;                                         // partial slot, -1: the tile is whole
+    int pad;
+
+    DSA_DEVINL uint32_t row0() const { return word & 255u; }
+    DSA_DEVINL uint32_t rows() const { return (word >> 8) & 255u; }
+    DSA_DEVINL bool is(uint32_t flag) const { return (word & flag) != 0; }
 };
 // First and last unit of the part; rows not yet summed; rows copied without TMA.
-enum : int { kUnitFirst = 1, kUnitLast = 2, kUnitFresh = 4, kUnitCopied = 8 };
+enum : uint32_t { kUnitFirst = 1u << 16, kUnitLast = 2u << 16, kUnitFresh = 4u << 16, kUnitCopied = 8u << 16 };
 
 struct MergeEntry { int tile, first_cta, parts, pad; };
 
@@ -144,43 +150,92 @@ constexpr uint32_t kPmAtom = kPmTile * 128;           // 64 channels of a slot's
 constexpr uint32_t kPmPBytes = kPmRows * 128;         // two P buffers, the halves of 128-byte rows
 static_assert(kPmQCol + kPmQSteps * 8 <= 512, "tensor memory columns");
 constexpr int kPmMaxSlots = 6;
+constexpr int kPmStages = 4;                          // E4M3 units in flight
+constexpr uint32_t kPmSleepNs = 100000;               // hint of a wait that may sleep
 
 struct PmCtl {
     uint64_t kv_full[kPmMaxSlots], kv_empty[kPmMaxSlots];
     uint64_t s_full[kPmSBufs], s_empty[kPmSBufs];
     uint64_t p_full[2], q_full, fin;
-    UnitInfo unit[kPmMaxSlots];
-    float alpha[kPmRows], linv[kPmRows];
+    uint64_t raw_full[kPmStages], raw_empty[kPmStages];
+    UnitInfo unit[kPmMaxSlots], raw_unit[kPmStages];
+    alignas(16) float alpha[kPmRows], linv[kPmRows];
+    // The plan: this CTA's first row tile and unit, its units, and for a row tile that
+    // it begins, the CTAs that hold it (0: worked out from per and begin).
     long long warp_sum[16];
     long long total, per, begin;
-    int first_tile, first_unit, first_units;
+    int first_tile, first_unit, first_units, count, parts;
+    int candidate[16];
+    TileWalk first;                                   // of first_tile
+    // The last part, written out by all warps.
+    int last_tile, last_part;
     uint32_t tmem_base;
     volatile int abort;
 };
 
-template <int kWidth>
+template <bool kFp8, int kWidth>
 struct PmSmem {
     static constexpr int kAtoms = kWidth / 64;
     static constexpr int kQAtoms = kAtoms - kPmQChannels / 64;      // of the queries, the others in tensor memory
-    static constexpr int kSlots = kWidth > DSA_KV_LORA ? 5 : 6;     // ring slots of one unit, as many as fit
+    // Ring slots of one unit, as many as fit beside the stages of E4M3 units.
+    static constexpr int kSlots = kFp8 ? (kWidth > DSA_KV_LORA ? 3 : 4) : (kWidth > DSA_KV_LORA ? 5 : 6);
     static constexpr uint32_t kQ = 0;                               // kQAtoms x [64 rows x 128 B]
     static constexpr uint32_t kKV = kQAtoms * kPmRows * 128;        // slots x kAtoms x [32 rows x 128 B]
     static constexpr uint32_t kSlot = kAtoms * kPmAtom;
     static constexpr uint32_t kP = kKV + kSlots * kSlot;
-    static constexpr uint32_t kCtl = kP + kPmPBytes;
+    static constexpr uint32_t kRaw = kP + kPmPBytes;                // stages x [32 rows x kWidth B]
+    static constexpr uint32_t kStage = kPmTile * kWidth;
+    static constexpr uint32_t kCtl = kRaw + (kFp8 ? kPmStages * kStage : 0);
     static constexpr int kBytes = (int)kCtl + (int)sizeof(PmCtl) + 1024;   // + alignment slack
 };
-static_assert(PmSmem<576>::kBytes <= 232448 && PmSmem<512>::kBytes <= 232448, "shared memory per block");
-static_assert(PmSmem<576>::kSlots <= kPmMaxSlots && PmSmem<512>::kSlots <= kPmMaxSlots, "ring");
+static_assert(PmSmem<false, 576>::kBytes <= 232448 && PmSmem<false, 512>::kBytes <= 232448 &&
+                  PmSmem<true, 576>::kBytes <= 232448 && PmSmem<true, 512>::kBytes <= 232448,
+              "shared memory per block");
+static_assert(PmSmem<false, 512>::kSlots <= kPmMaxSlots, "ring");
 static_assert(65535 * 2 <= (int)(kPmPBytes / 8) * kPmThreads, "block sums hold every row tile");
 
+// Bounded wait of a warp that may sleep: the hint lets the hardware hold the warp
+// until the phase completes instead of answering "not yet" at once, since a dozen
+// polling warps fill the queue to shared memory that every exchange, barrier and
+// global store of the working warps goes through.
+DSA_DEVINL bool pm_try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kPmSleepNs)
+        : "memory");
+    return ok != 0;
+}
+
+// Two probes whose answers are waited for together: bit i is set when barrier i's phase
+// of the given parity has completed, for every lane of the warp.
+DSA_DEVINL uint32_t pm_test2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 a, b;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "selp.u32 a, 1, 0, p;\n\tselp.u32 b, 2, 0, q;\n\tor.b32 %0, a, b;\n\t}"
+        : "=r"(r)
+        : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
+        : "memory");
+    return __reduce_and_sync(0xffffffffu, r);
+}
+
 DSA_DEVINL bool pm_wait(PmCtl *ctl, uint64_t *bar, uint32_t parity) {
-    if (ctl->abort) return false;
-    if (!mbar_wait(bar, parity)) {
-        ctl->abort = 1;
-        return false;
+    if (pm_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (pm_try_wait(bar, parity)) return true;
+        if (ctl->abort) return false;
+        if (clock64() - t0 > kWaitLimitCycles) break;
     }
-    return true;
+    raise_device_error(kErrWaitTimeout);
+    ctl->abort = 1;
+    return false;
 }
 
 // One lane of a converged warp, chosen so that the compiler knows it is one:
@@ -192,6 +247,20 @@ DSA_DEVINL bool elect_one() {
     return p != 0;
 }
 
+// Four E4M3 codes (low byte first) widened to bf16 pairs by integer moves and one
+// multiplication: exponent and mantissa shifted to bf16's places give the value
+// times 2^-120, subnormals included, and the product with 2^120 is exact. NaN codes
+// (S.1111.111) would become 480: the result has bit 7 of their bytes set (adding 1
+// to seven ones is the one sum that carries; other bits mean nothing).
+DSA_DEVINL uint32_t e4m3x4_to_bf16x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    const uint32_t mag = v & 0x7F7F7F7Fu;
+    const uint32_t x = (__byte_perm(v, 0, 0x1404) & 0x80008000u) | (__byte_perm(mag, 0, 0x4140) << 4);
+    const uint32_t y = (__byte_perm(v, 0, 0x3424) & 0x80008000u) | (__byte_perm(mag, 0, 0x4342) << 4);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7B807B80u));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7B807B80u));
+    return mag + 0x01010101u;
+}
+
 DSA_DEVINL long long warp_inclusive_sum(long long v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -201,66 +270,185 @@ DSA_DEVINL long long warp_inclusive_sum(long long v, int lane) {
     return v;
 }
 
-// The plan: units of all row tiles in order, cut into equal ranges of `per`
-// units, one a CTA (a row tile split over CTAs leaves partial results; a CTA
-// leaves at most two, one of its first and one of its last row tile). Every CTA
-// works it out from the lengths on the device, so nothing depends on the host's
-// bounds, and ragged batches load every SM alike. block_sum: shared scratch, one
-// sum for every 512 row tiles.
-DSA_DEVINL void pm_plan(PmCtl *ctl, long long *block_sum, const PrefixGeom &g, const RowTiles &rt, int P) {
+// The plan, worked out by every CTA from the lengths on the device, so that
+// nothing depends on the host's bounds and ragged batches load every SM alike.
+// The units of all row tiles in order are cut into equal ranges of `per` units,
+// one a CTA; a row tile split over CTAs leaves partial results, of which a CTA
+// then leaves at most two, one of its first and one of its last row tile. Where
+// there are fewer row tiles than CTAs, whole CTAs are given to each instead if
+// the longest range grows by less than a second part costs (its queries, its
+// output: kPmPartUnits). scratch: shared, 8 KB.
+DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const RowTiles &rt, int P) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kPmThreads / 32;
     const int nb = (rt.count + kPmThreads - 1) / kPmThreads;
-    for (int k = tid; k < nb; k += kPmThreads) block_sum[k] = 0;
-    __syncthreads();
+    const int G = (int)gridDim.x;
     TileWalk w;
     int units = 0;
-    for (int k = 0; k < nb; ++k) {
-        const int t = k * kPmThreads + tid;
-        units = 0;
-        if (t < rt.count) {
-            w.load(g, rt, t, P);
+    long long base = 0, total = 0, inc;
+    int kb = 0;
+    if (nb == 1) {
+        if (tid < rt.count) {
+            w.load(g, rt, tid, P);
             units = w.units;
         }
-        long long s = units;
+        if (tid < kPmGrid) reinterpret_cast<int *>(scratch)[tid] = units;
+        inc = warp_inclusive_sum(units, lane);
+        if (lane == 31) ctl->warp_sum[warp] = inc;
+        if (tid == 0) ctl->count = ctl->parts = 0;
+        __syncthreads();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0 && s)
-            atomicAdd(reinterpret_cast<unsigned long long *>(&block_sum[k]), (unsigned long long)s);
+        for (int k = 0; k < kWarps; ++k) {
+            base += k < warp ? ctl->warp_sum[k] : 0;
+            total += ctl->warp_sum[k];
+        }
+    } else {
+        auto *block_sum = reinterpret_cast<long long *>(scratch);
+        for (int k = tid; k < nb; k += kPmThreads) block_sum[k] = 0;
+        if (tid == 0) ctl->count = ctl->parts = 0;
+        __syncthreads();
+        for (int k = 0; k < nb; ++k) {
+            const int t = k * kPmThreads + tid;
+            units = 0;
+            if (t < rt.count) {
+                w.load(g, rt, t, P);
+                units = w.units;
+            }
+            long long s = units;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0 && s)
+                atomicAdd(reinterpret_cast<unsigned long long *>(&block_sum[k]), (unsigned long long)s);
+        }
+        __syncthreads();
+        for (int k = 0; k < nb; ++k) total += block_sum[k];
     }
-    __syncthreads();
-    long long total = 0;
-    for (int k = 0; k < nb; ++k) total += block_sum[k];
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kPmMinUnits);
+    // a range shorter than kPmMinUnits is not worth its part; with more row tiles than
+    // CTAs it is not the splitting that makes ranges short
+    const long long per = max((total + G - 1) / G, (long long)(rt.count <= G ? kPmMinUnits : 1));
     const long long begin = per * blockIdx.x;
     if (tid == 0) {
         ctl->total = total;
         ctl->per = per;
         ctl->begin = begin;
     }
+    if (rt.count > 1 && rt.count <= G && total < (1 << 30)) {
+        // Candidates for the longest range, one a warp, from `per` up to one that is
+        // sure to fit: total / hi + count <= G.
+        const auto *tile_units = reinterpret_cast<const int *>(scratch);
+        const int lo = (int)per;
+        const int hi = rt.count < G ? max(lo, ((int)total + G - rt.count - 1) / (G - rt.count)) : (int)total;
+        const int mine = lo + (int)((long long)(hi - lo) * warp / (kWarps - 1));
+        int ctas = 0;
+        for (int t = lane; t < rt.count; t += 32) ctas += (tile_units[t] + mine - 1) / mine;
+        ctas = __reduce_add_sync(0xffffffffu, ctas);
+        if (lane == 0) ctl->candidate[warp] = ctas <= G ? mine : INT32_MAX;
+        __syncthreads();
+        int best = INT32_MAX;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) best = min(best, ctl->candidate[k]);
+        if (best - lo < kPmPartUnits) {
+            if (warp == 0) {
+                // lane l: five consecutive row tiles; the CTAs before and in each
+                constexpr int kEach = (kPmGrid + 31) / 32;
+                int need[kEach], sum = 0;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int t = lane * kEach + i;
+                    need[i] = t < rt.count ? (tile_units[t] + best - 1) / best : 0;
+                    sum += need[i];
+                }
+                int before = (int)warp_inclusive_sum(sum, lane) - sum;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int b = (int)blockIdx.x - before;
+                    if (b >= 0 && b < need[i]) {
+                        const int t = lane * kEach + i, u = tile_units[t];
+                        const int each = (u + need[i] - 1) / need[i];
+                        ctl->first_tile = t;
+                        w.load(g, rt, t, P);
+                        ctl->first = w;
+                        ctl->first_unit = min(u, b * each);
+                        ctl->first_units = u;
+                        ctl->count = max(0, min(each, u - b * each));
+                        ctl->parts = (u + each - 1) / each;
+                    }
+                    before += need[i];
+                }
+            }
+            __syncthreads();
+            return;
+        }
+    }
     if (begin < total) {
-        long long base = 0;
-        int kb = 0;
-        while (base + block_sum[kb] <= begin) base += block_sum[kb++];
         if (nb > 1) {
+            const auto *block_sum = reinterpret_cast<const long long *>(scratch);
+            while (base + block_sum[kb] <= begin) base += block_sum[kb++];
             const int t = kb * kPmThreads + tid;
             units = 0;
             if (t < rt.count) {
                 w.load(g, rt, t, P);
                 units = w.units;
             }
+            inc = warp_inclusive_sum(units, lane);
+            if (lane == 31) ctl->warp_sum[warp] = inc;
+            __syncthreads();
+            for (int k = 0; k < warp; ++k) base += ctl->warp_sum[k];
         }
-        const long long inc = warp_inclusive_sum(units, lane);
-        if (lane == 31) ctl->warp_sum[warp] = inc;
-        __syncthreads();
-        for (int k = 0; k < warp; ++k) base += ctl->warp_sum[k];
-        const long long lo = base + inc - units;
-        if (units > 0 && lo <= begin && begin < lo + units) {
+        const long long first = base + inc - units;
+        if (units > 0 && first <= begin && begin < first + units) {
             ctl->first_tile = kb * kPmThreads + tid;
-            ctl->first_unit = (int)(begin - lo);
+            ctl->first = w;
+            ctl->first_unit = (int)(begin - first);
             ctl->first_units = units;
+            ctl->count = (int)min((long long)INT32_MAX, min(per, total - begin));
         }
     }
     __syncthreads();
+}
+
+// One of the eight pieces (128-channel block blk / 2, 32-row half blk % 2) of O^T in a
+// lane quarter, out of tensor memory: normalised bf16 rows, or a part's fp32 rows.
+DSA_DEVINL void pm_write_rows(const PmCtl *ctl, uint32_t tquarter, int quarter, int blk, int nr, size_t row0,
+                              int part_slot, __nv_bfloat16 *out, float *part) {
+    const int lane = threadIdx.x & 31;
+    uint32_t o[32];
+    tc::tmem_ld32(tquarter + (blk >> 1) * 64 + (blk & 1) * 32, o);
+    tc::tmem_wait_ld();
+    const int L = (blk >> 1) * 128 + 32 * quarter + lane, r0 = (blk & 1) * 32;
+    if (part_slot >= 0) {
+        float *po = part + ((size_t)part_slot * kPmRows + r0) * kL + L;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (r0 + j < nr) po[(size_t)j * kL] = __uint_as_float(o[j]);
+        return;
+    }
+    // All factors are read before the first store, which the compiler must take for one
+    // that could change them. A row that saw nothing is 0 whatever its column holds.
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(&ctl->linv[r0 + j]);
+        const float inv[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[j + k] = inv[k] != 0.f ? __float_as_uint(__uint_as_float(o[j + k]) * inv[k]) : 0u;
+    }
+    // Lanes 2i and 2i+1 hold channels L, L+1: the even lane writes both channels of
+    // row j, the odd lane those of row j+1. Exchanges first, then stores: an exchange
+    // is not moved before a store, and would wait out its latency sixteen times.
+    const bool odd = lane & 1;
+    uint32_t v[16];
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float x = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? o[j] : o[j + 1], 1));
+        const float y = __uint_as_float(odd ? o[j + 1] : o[j]);
+        v[j / 2] = odd ? pack_bf16x2(x, y) : pack_bf16x2(y, x);
+    }
+    const int first = r0 + (odd ? 1 : 0);
+    __nv_bfloat16 *ob = out + (row0 + first) * kL + (L & ~1);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2)
+        if (first + j < nr) *reinterpret_cast<uint32_t *>(ob + (size_t)j * kL) = v[j / 2];
 }
 
 // kv: kv_rows rows of kWidth bf16, or E4M3 bytes (kFp8; widened to bf16, which
@@ -273,7 +461,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                   float *__restrict__ part, float2 *__restrict__ part_ml,
                   MergeEntry *__restrict__ merge, __nv_bfloat16 *__restrict__ out,
                   float *__restrict__ lse) {
-    using S = PmSmem<kWidth>;
+    using S = PmSmem<kFp8, kWidth>;
     constexpr int kAtoms = S::kAtoms, kPmSlots = S::kSlots;
     extern __shared__ uint8_t pm_smem_raw[];
     const uint32_t raw = smem_u32(pm_smem_raw);
@@ -291,7 +479,8 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     }
     if (tid == 0) {
         for (int i = 0; i < kPmSlots; ++i) {
-            mbar_init(&ctl->kv_full[i], 4 * 32 + 4);  // four warps' lanes' copies + a word from each warp
+            // four warps: a word from each, and where lanes copy rows, every lane's copies
+            mbar_init(&ctl->kv_full[i], kFp8 ? 4 : 4 * 32 + 4);
             mbar_init(&ctl->kv_empty[i], 1);
         }
         for (int i = 0; i < kPmSBufs; ++i) {
@@ -301,9 +490,14 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->p_full[i], 128);
         }
+        for (int i = 0; i < kPmStages; ++i) {
+            mbar_init(&ctl->raw_full[i], 1);
+            mbar_init(&ctl->raw_empty[i], 4);
+        }
         mbar_init(&ctl->q_full, 128);
         mbar_init(&ctl->fin, 2);
         ctl->abort = 0;
+        ctl->last_tile = -1;
         fence_mbarrier_init();
     }
     tc::fence_before_sync();
@@ -314,8 +508,8 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     pdl_launch_dependents();
 
     const int P = g.shared_len();
-    pm_plan(ctl, reinterpret_cast<long long *>(gbase + S::kP), g, rt, P);
-    const int n = (int)min((long long)INT32_MAX, max(0ll, min(ctl->per, ctl->total - ctl->begin)));
+    pm_plan(ctl, gbase + S::kP, g, rt, P);
+    const int n = ctl->count;
     const bool by_tile = rt.count <= kPmGrid;
     if (!by_tile && tid == 0) {
         // merge entries by CTA: the second CTA of a split row tile holds it
@@ -342,12 +536,12 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         for (int c = 0; c < n; ++c) {
             const int sb = c % kPmSBufs;
             ok = pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
-            const int flags = ctl->unit[slot].flags;
+            const uint32_t word = ctl->unit[slot].word;
             if (ok && c >= kPmSBufs) ok = pm_wait(ctl, &ctl->s_empty[sb], ((c / kPmSBufs) - 1) & 1);
-            if (ok && (flags & kUnitFirst)) ok = pm_wait(ctl, &ctl->q_full, parts++ & 1);
+            if (ok && (word & kUnitFirst)) ok = pm_wait(ctl, &ctl->q_full, parts++ & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after_sync();
-            if (flags & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
+            if (word & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
             if (elect_one()) {
                 const uint32_t d = tmem + kPmSCol + (uint32_t)(sb * kPmTile);
                 const uint64_t b0 = tc::desc_sw128(sKV + slot * S::kSlot, 16, 1024);
@@ -381,15 +575,14 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         for (int c = 0; c < n; ++c) {
             const int pb = c & 1;
             ok = pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
-            const uint32_t rows = (uint32_t)__shfl_sync(0xffffffffu, ctl->unit[slot].rows, 0);
-            const uint32_t flags = (uint32_t)__shfl_sync(0xffffffffu, ctl->unit[slot].flags, 0);
-            const uint32_t row0 = rows & 255u;
+            const uint32_t word = __shfl_sync(0xffffffffu, ctl->unit[slot].word, 0);
+            const uint32_t row0 = word & 255u;
             if (ok) ok = pm_wait(ctl, &ctl->p_full[pb], (c >> 1) & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after_sync();
-            if (flags & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
+            if (word & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
             if (elect_one()) {
-                const uint32_t id = tc::idesc_bf16(128, 0, true, false) | ((rows >> 8) >> 3 << 17);
+                const uint32_t id = tc::idesc_bf16(128, 0, true, false) | (((word >> 8) & 255u) >> 3 << 17);
                 // V^T: MN-major, 64-channel atoms kPmAtom apart, 8-token groups 1 KB apart
                 const uint64_t a0 = tc::desc_sw128(sKV + slot * S::kSlot, kPmAtom, 1024);
                 // P^T: K-major, 128-byte rows (this buffer's half), 8-row groups 1 KB apart
@@ -401,7 +594,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                         tc::mma_bf16_ss(tmem + (uint32_t)(blk * kPmRows) + row0,
                                         a0 + (uint64_t)((blk * 2 * kPmAtom + ks * 2048) >> 4),
                                         b0 + (uint64_t)((ks * 32) >> 4), id,
-                                        (ks > 0 || !(flags & kUnitFresh)) ? 1u : 0u);
+                                        (ks > 0 || !(word & kUnitFresh)) ? 1u : 0u);
                 tc::mma_commit(&ctl->kv_empty[slot]);
             }
             __syncwarp();
@@ -410,92 +603,181 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         __syncwarp();
         if (elect_one()) tc::mma_commit(&ctl->fin);
         __syncwarp();
-    } else if (warp >= 4) {
-        // ------------------------------------------------------------------ loaders (warps 4-11)
-        // Two groups of four warps fill alternate units. Lane l of every warp finds
+    } else if (kFp8 && warp >= 4 && warp < 12) {
+        // ------------------------------------------------------------------ widening (E4M3, warps 4-11)
+        // Two groups of four warps take alternate units from the stages, widen them to
+        // bf16 exactly, eight rows a warp, and store them into the swizzled slots; rows
+        // where there is no token become zeros. Eight codes make one 16-byte column of a
+        // slot's row: lane l takes columns l and l + 32, so that neither access conflicts.
+        const int sub = (warp - 4) & 3;
+        constexpr int kCols = kWidth / 8, kLoads = 8 * kCols / 32;         // 16 or 18 a lane
+        for (int c = (warp - 4) >> 2; c < n; c += 2) {
+            const int slot = c % kPmSlots, stage = c % kPmStages;
+            bool ok = pm_wait(ctl, &ctl->raw_full[stage], (c / kPmStages) & 1);
+            const UnitInfo info = ctl->raw_unit[stage];
+            const uint8_t *src = gbase + S::kRaw + stage * S::kStage;
+            const uint32_t dst0 = sKV + slot * S::kSlot;
+            // columns l and l + 32 of row i, then columns 64 .. 71 of four rows a time
+            auto row_of = [&](int i) { return 8 * sub + (i < 16 ? i >> 1 : 4 * (i - 16) + (lane >> 3)); };
+            auto col_of = [&](int i) { return i < 16 ? lane + 32 * (i & 1) : 64 + (lane & 7); };
+            uint2 x[kLoads];
+            uint32_t nan = 0;                         // bit 7 of every byte: a NaN code was there
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = row_of(i);
+                x[i] = (info.valid >> r) & 1u ? *reinterpret_cast<const uint2 *>(src + r * kWidth + 8 * col_of(i))
+                                              : make_uint2(0u, 0u);
+            }
+            if (ok && c >= kPmSlots) ok = pm_wait(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            auto store = [&](int i, const uint32_t (&w)[4]) {
+                const int r = row_of(i), cc = col_of(i);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 dst0 + (cc >> 3) * kPmAtom + r * 128 + (((cc & 7) ^ (r & 7)) << 4)),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+            };
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                uint32_t w[4];
+                nan |= e4m3x4_to_bf16x4(x[i].x, w[0], w[1]);
+                nan |= e4m3x4_to_bf16x4(x[i].y, w[2], w[3]);
+                store(i, w);
+            }
+            if (nan & 0x80808080u) {
+                // some code of this lane was NaN: its columns again by the conversion instruction
+#pragma unroll 1
+                for (int i = 0; i < kLoads; ++i) {
+                    const int r = row_of(i);
+                    if (!((info.valid >> r) & 1u)) continue;
+                    const uint2 v = *reinterpret_cast<const uint2 *>(src + r * kWidth + 8 * col_of(i));
+                    const uint32_t w[4] = {e4m3x2_to_bf16x2((uint16_t)(v.x & 0xFFFFu)),
+                                           e4m3x2_to_bf16x2((uint16_t)(v.x >> 16)),
+                                           e4m3x2_to_bf16x2((uint16_t)(v.y & 0xFFFFu)),
+                                           e4m3x2_to_bf16x2((uint16_t)(v.y >> 16))};
+                    store(i, w);
+                }
+            }
+            tc::fence_proxy_async_smem();               // generic stores -> tensor-core reads
+            __syncwarp();
+            if (lane == 0) {
+                if (sub == 0) ctl->unit[slot] = info;
+                mbar_arrive(&ctl->kv_full[slot]);
+                mbar_arrive(&ctl->raw_empty[stage]);
+            }
+            __syncwarp();
+        }
+    } else if (kFp8 ? warp >= kPmIssuer + 2 : warp >= 4 && warp < 12) {
+        // ------------------------------------------------------------------ loaders
+        // bf16: two groups of four warps fill alternate units of the ring; E4M3: two
+        // warps fill alternate stages. Lane l of every warp finds
         // the cache row of the unit's token l. Where the 32 rows are whole boxes of
         // the tensor map (pages that are a multiple of 16 rows, away from the ends
         // of a segment) one thread brings them by TMA; else warp i of the group
         // copies rows 8i .. 8i+7 in 16-byte pieces, zero-filled where there is no
         // token: what lies behind a sequence may hold anything, and a weight of 0
         // times a NaN would not be 0.
-        const int grp = (warp - 4) >> 2, sub = (warp - 4) & 3;
+        const int grp = kFp8 ? warp - kPmIssuer - 2 : (warp - 4) >> 2, sub = kFp8 ? 0 : (warp - 4) & 3;
         TileWalk w;
         int tile = n > 0 ? ctl->first_tile : 0, u = n > 0 ? ctl->first_unit : 0;
         int part_begin = u;                               // the part's first unit in its tile
-        if (n > 0) w.load(g, rt, tile, P);
+        if (n > 0) w = ctl->first;
         long long global_unit = ctl->begin;
         int left = n;                                     // units from the current one on
-
+        // The segment of the current unit: query seg (-1: the prefix), its tokens s0 .. s1-1,
+        // the unit's first token, the units from this one to the segment's end, whether the
+        // unit is the segment's first; and for the row lookups the request's table.
+        int seg = -1, s0 = 0, s1 = 0, tok0 = 0, seg_left = 0;
+        bool seg_first = false;
+        uint32_t rows_word = 0;
+        const int32_t *pages = nullptr;
+        // the unit `skip` units behind the start of segment k of the tile, or of a later one
+        auto enter_segment = [&](int k, int skip) {
+            for (;; ++k) {
+                int nu = k < 0 ? w.npre : 0;
+#pragma unroll
+                for (int i = 0; i < kPmQueries; ++i)
+                    if (k == i && i < w.nq) nu = w.query_units(i, P);
+                if (skip < nu || k >= w.nq) {
+                    seg_left = nu - skip;
+                    break;
+                }
+                skip -= nu;
+            }
+            seg = k;
+            seg_first = skip == 0;
+            s0 = k >= 0 && w.shared ? P : 0;
+            s1 = k < 0 ? P : 0;
+            int b = 0;
+#pragma unroll
+            for (int i = 0; i < kPmQueries; ++i)
+                if (k == i) { s1 = w.vis[i]; b = w.req[i]; }
+            if (w.active == 0) { s1 = 0; b = 0; seg_left = 1; }   // no query sees a token: an empty unit
+            pages = g.block_table + (size_t)b * g.max_blocks;
+            tok0 = (int)((unsigned)s0 / kPmTile * kPmTile) + skip * kPmTile;
+            rows_word = (k < 0 || rt.qpt == 1 || w.active == 0 ? (uint32_t)kPmRows << 8
+                                                              : (uint32_t)(k * Hm) | ((uint32_t)Hm << 8)) |
+                        ((uint32_t)w.active << 24);
+        };
         // describe the current unit; returns the row of this lane's token
         auto describe = [&](UnitInfo &info) -> int {
-            int seg_unit = u, k = -1, s0 = 0, s1 = P, rows0 = 0, rowsn = kPmRows, b = 0;
-            if (u >= w.npre) {
-                seg_unit = u - w.npre;
-                k = 0;
-#pragma unroll
-                for (int i = 0; i < kPmQueries - 1; ++i) {
-                    const int nu = i < w.nq ? w.query_units(i, P) : 0;
-                    if (k == i && i + 1 < w.nq && seg_unit >= nu) {
-                        seg_unit -= nu;
-                        k = i + 1;
-                    }
-                }
-                s0 = w.shared ? P : 0;
-                s1 = w.vis[0];
-                b = w.req[0];
-#pragma unroll
-                for (int i = 1; i < kPmQueries; ++i)
-                    if (k == i) { s1 = w.vis[i]; b = w.req[i]; }
-                if (rt.qpt > 1) { rows0 = k * Hm; rowsn = Hm; }
-            }
-            const int tok0 = (k < 0 ? 0 : s0 / kPmTile * kPmTile) + seg_unit * kPmTile;
-            const int part_last = min(w.units, u + left) - 1;
-            const bool none = w.active == 0;              // no query sees a token: an empty unit
-            if (none) { rows0 = 0; rowsn = kPmRows; }
-            info.rows = rows0 | (rowsn << 8);
-            const bool pre_seen = w.shared && part_begin < w.npre;
-            const bool fresh = u == part_begin || (k >= 0 && seg_unit == 0 && !pre_seen);
-            info.flags = (u == part_begin ? kUnitFirst : 0) | (u == part_last ? kUnitLast : 0) |
-                         (fresh ? kUnitFresh : 0) | (w.active << 8);
-            const bool whole = part_begin == 0 && part_last == w.units - 1;
-            info.part = whole ? -1 : 2 * (int)blockIdx.x + (part_begin == 0 ? 1 : 0);
+            const bool first = u == part_begin, last = left == 1 || u + 1 == w.units;
+            const bool fresh = first || (seg >= 0 && seg_first && !(w.shared && part_begin < w.npre));
+            info.word = rows_word | (first ? kUnitFirst : 0u) | (last ? kUnitLast : 0u) | (fresh ? kUnitFresh : 0u);
+            // read on the last unit alone: a part that is the whole tile has no slot
+            info.part = part_begin == 0 && u + 1 == w.units ? -1 : 2 * (int)blockIdx.x + (part_begin == 0 ? 1 : 0);
             const int t = tok0 + lane;
-            int row = -1;
-            if (!none && t >= s0 && t < s1) row = g.row(b, t, P);
-            info.valid = __ballot_sync(0xffffffffu, row >= 0);
-            if (by_tile && u == 0 && sub == 0 && lane == 0) {
-                // merge entries by row tile, left by the CTA that begins it
-                const int cf = (int)(global_unit / ctl->per);
-                const int cl = (int)((global_unit + w.units - 1) / ctl->per);
-                merge[tile] = MergeEntry{tile, cf, cl - cf + 1, 0};
+            return t >= s0 && t < s1 ? g.row(pages, t, P) : -1;
+        };
+        // merge entries by row tile, left by the CTA that begins it
+        auto enter_tile = [&]() {
+            if (by_tile && grp == 0 && sub == 0 && lane == 0) {
+                const int parts = ctl->parts ? ctl->parts
+                                             : (int)((global_unit + w.units - 1) / ctl->per) - (int)blockIdx.x + 1;
+                merge[tile] = MergeEntry{tile, (int)blockIdx.x, parts, 0};
             }
-            return row;
         };
         // one unit forward; false behind the last
         auto advance = [&]() -> bool {
             if (--left <= 0) return false;
             ++global_unit;
-            if (++u >= w.units) {
+            ++u;
+            tok0 += kPmTile;
+            seg_first = false;
+            if (--seg_left > 0) return true;
+            if (u >= w.units) {
                 u = 0;
                 part_begin = 0;
                 w.load(g, rt, ++tile, P);
+                enter_tile();
+                enter_segment(w.npre > 0 ? -1 : 0, 0);
+            } else {
+                enter_segment(seg + 1, 0);
             }
             return true;
         };
 
+        if (n > 0) {
+            if (u == 0) enter_tile();
+            enter_segment(w.npre > 0 ? -1 : 0, u);
+        }
         bool more = n > 0;
         if (grp == 1) more = more && advance();
+        int slot = grp;
+        uint32_t ph = 1;                                  // parity of the slot's last release
+        auto next_slot = [&]() {
+            slot += 2;
+            if (slot >= kPmSlots) { slot -= kPmSlots; ph ^= 1u; }
+        };
         UnitInfo info;
         int row = -1;
         if (more) row = describe(info);
-        for (int c = grp; more; c += 2) {
-            const int slot = c % kPmSlots;
-            const uint32_t dst0 = sKV + slot * S::kSlot;
-            bool ok = true;
-            if constexpr (!kFp8) {
-                if (c >= kPmSlots) ok = pm_wait(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
+        if constexpr (!kFp8) {
+            for (int c = grp; more; c += 2, next_slot()) {
+                const uint32_t dst0 = sKV + slot * S::kSlot;
+                const bool ok = c < kPmSlots || pm_wait(ctl, &ctl->kv_empty[slot], ph);
                 if (!__all_sync(0xffffffffu, ok)) break;
+                info.valid = __ballot_sync(0xffffffffu, row >= 0);
                 bool boxes = box_rows > 0 && info.valid == 0xffffffffu;
                 if (boxes) {
                     const int first = __shfl_sync(0xffffffffu, row, lane & ~(box_rows - 1));
@@ -552,59 +834,50 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                         }
                     }
                     if (lane == 0) {
-                        info.flags |= kUnitCopied;
+                        info.word |= kUnitCopied;
                         if (sub == 0) ctl->unit[slot] = info;
                         mbar_arrive(&ctl->kv_full[slot]);
                     }
                     tc::cp_async_arrive_noinc(&ctl->kv_full[slot]);
                 }
-            } else {
-                // E4M3 rows: 16-byte pieces (16 channels) of the warp's 8 rows, all loads
-                // in flight before the slot is free, then widened to bf16 exactly.
-                constexpr int kPieces = kWidth / 16;                       // 32 or 36 a row
-                constexpr int kLoads = (8 * kPieces + 31) / 32;            // 8 or 9 a lane
-                const auto *kv8 = reinterpret_cast<const uint8_t *>(kv);
-                uint4 raw16[kLoads];
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    // pieces 0..31 of row i, then pieces 32..35 of the eight rows
-                    const int r = 8 * sub + (i < 8 ? i : lane >> 2);
-                    const int pc = i < 8 ? lane : 32 + (lane & 3);
-                    const int src_row = __shfl_sync(0xffffffffu, row, r);
-                    raw16[i] = src_row >= 0 ? ldg_nc_v4(kv8 + (size_t)src_row * kWidth + 16 * pc)
-                                            : make_uint4(0u, 0u, 0u, 0u);
-                }
-                if (c >= kPmSlots) ok = pm_wait(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int r = 8 * sub + (i < 8 ? i : lane >> 2);
-                    const int pc = i < 8 ? lane : 32 + (lane & 3);
-                    const uint32_t x[4] = {raw16[i].x, raw16[i].y, raw16[i].z, raw16[i].w};
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int cc = 2 * pc + hh;                        // 16-byte piece of the bf16 row
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         dst0 + (cc >> 3) * kPmAtom + r * 128 + (((cc & 7) ^ (r & 7)) << 4)),
-                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh] & 0xFFFFu))),
-                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh] >> 16))),
-                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh + 1] & 0xFFFFu))),
-                                     "r"(e4m3x2_to_bf16x2((uint16_t)(x[2 * hh + 1] >> 16)))
-                                     : "memory");
-                    }
-                }
-                tc::fence_proxy_async_smem();               // generic stores -> tensor-core reads
-                if (lane == 0) {
-                    if (sub == 0) ctl->unit[slot] = info;
-                    mbar_arrive(&ctl->kv_full[slot]);
-                }
-                mbar_arrive(&ctl->kv_full[slot]);
+                more = advance() && advance();
+                if (more) row = describe(info);           // its page lookups run behind this unit's copies
             }
-            more = advance() && advance();
-            if (more) row = describe(info);               // its page lookups run behind this unit's copies
+        } else {
+            // A unit's rows lie one after the other within a page: one bulk copy for 32
+            // rows of one page, two for halves, else one a row.
+            const auto *kv8 = reinterpret_cast<const uint8_t *>(kv);
+            for (int c = grp; more; c += 2) {
+                const int stage = c % kPmStages;
+                const bool ok = c < kPmStages || pm_wait(ctl, &ctl->raw_empty[stage], ((c / kPmStages) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                info.valid = __ballot_sync(0xffffffffu, row >= 0);
+                const int head = __shfl_sync(0xffffffffu, row, lane & 16);
+                const int row_a = __shfl_sync(0xffffffffu, row, 0);
+                const bool halves = __all_sync(0xffffffffu, row >= 0 && row == head + (lane & 15));
+                const bool whole = halves && __all_sync(0xffffffffu, row == row_a + lane);
+                uint8_t *dst = gbase + S::kRaw + stage * S::kStage;
+                if (elect_one()) {
+                    ctl->raw_unit[stage] = info;
+                    mbar_arrive_expect_tx(&ctl->raw_full[stage], __popc(info.valid) * kWidth);
+                    if (whole) bulk_g2s(dst, kv8 + (size_t)row_a * kWidth, kPmTile * kWidth, &ctl->raw_full[stage]);
+                }
+                __syncwarp();
+                if (!whole) {
+                    if (halves) {
+                        if ((lane & 15) == 0)
+                            bulk_g2s(dst + lane * kWidth, kv8 + (size_t)row * kWidth, 16 * kWidth, &ctl->raw_full[stage]);
+                    } else if (row >= 0) {
+                        bulk_g2s(dst + lane * kWidth, kv8 + (size_t)row * kWidth, kWidth, &ctl->raw_full[stage]);
+                    }
+                    __syncwarp();
+                }
+                more = advance() && advance();
+                if (more) row = describe(info);
+            }
         }
         tc::cp_async_wait_all();          // nothing of this warp in flight past here
-    } else {
+    } else if (warp < 4) {
         // ------------------------------------------------------------------ softmax (warps 0-3)
         // S is read with the 16x64b tensor-memory shape: thread t of warp wq holds
         // row hh = 16 wq + (t>>2) + 8 (t&1) and the unit's tokens of parity
@@ -633,10 +906,15 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 else
                     tc::st_shared_zero16(dst);
             }
+            // All rows are asked for at once; the batches below then wait for L2 and not
+            // three times for memory.
+            for (int x = wtid; x < nr * (kPmQChannels / 64); x += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (size_t)(row0 + x / (kPmQChannels / 64)) * kWidth +
+                                                              x % (kPmQChannels / 64) * 64));
             const uint4 *src = reinterpret_cast<const uint4 *>(q + (size_t)(row0 + min(hh, nr - 1)) * kWidth) + par;
-            constexpr int kBatch = kPmQSteps * 8 / 32 / 2;    // 32-column blocks in flight
+            constexpr int kBatches = 3, kBatch = kPmQSteps * 8 / 32 / kBatches;   // 32-column blocks in flight
 #pragma unroll
-            for (int b0 = 0; b0 < 2; ++b0) {
+            for (int b0 = 0; b0 < kBatches; ++b0) {
                 uint4 v[kBatch][4];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b)
@@ -696,16 +974,13 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             tc::tmem_ld16x64b_x16(tl + kPmSCol + (uint32_t)(sb * kPmTile), sr);
             // What the end of this turn needs, asked for while the scores arrive: shared
             // memory answers slowly while the tensor cores read their operands.
-            const bool next_ready = c + 1 < n && mbar_test(&ctl->kv_full[nslot], npar);
-            const bool p_free = c < 2 || mbar_test(&ctl->kv_empty[slot2], par2);
+            const uint32_t ready = pm_test2(&ctl->kv_full[nslot], npar, &ctl->kv_empty[slot2], par2);
             tc::tmem_wait_ld();
             tc::fence_before_sync();
             mbar_arrive(&ctl->s_empty[sb]);
-            UnitInfo next = info;
-            if (next_ready) next = ctl->unit[nslot];
+            UnitInfo next = ctl->unit[nslot];             // the next unit's once it is ready
 
-            const int urow0 = info.rows & 255;
-            const bool mine = hh >= urow0 && hh < urow0 + (info.rows >> 8) && ((info.flags >> (8 + hq)) & 1);
+            const bool mine = (uint32_t)hh - info.row0() < info.rows() && ((info.word >> (24 + hq)) & 1u);
             const uint32_t vm = mine ? info.valid >> par : 0u;
             float z[16];
 #pragma unroll
@@ -723,7 +998,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             bool moved = false;
             if (mx > m_used + kLazyRescale) {
                 // nothing summed before: nothing to rescale
-                moved = m_used != -INFINITY && !(info.flags & kUnitFirst);
+                moved = m_used != -INFINITY && !info.is(kUnitFirst);
                 alpha = ex2(m_used - mx);
                 m_used = mx;
             }
@@ -746,7 +1021,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 const float recv = __shfl_xor_sync(0xffffffffu, par ? z[k] : z[k + 8], 2);
                 pk[k] = par ? pack_bf16x2(recv, z[k + 8]) : pack_bf16x2(z[k], recv);
             }
-            if (!p_free) bad = bad || !pm_wait(ctl, &ctl->kv_empty[slot2], par2);
+            if (c >= 2 && !(ready & 2u)) bad = bad || !pm_wait(ctl, &ctl->kv_empty[slot2], par2);
             // One barrier a unit; a second only when some row rescales or a wait failed.
             const bool need = tc::named_bar_or(2, 128, bad || moved);
             if (need) {
@@ -773,8 +1048,13 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                     tc::tmem_ld32(ta, o);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        o[j] = __float_as_uint(__uint_as_float(o[j]) * ctl->alpha[(blk & 1) * 32 + j]);
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&ctl->alpha[(blk & 1) * 32 + j]);
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * f.x);
+                        o[j + 1] = __float_as_uint(__uint_as_float(o[j + 1]) * f.y);
+                        o[j + 2] = __float_as_uint(__uint_as_float(o[j + 2]) * f.z);
+                        o[j + 3] = __float_as_uint(__uint_as_float(o[j + 3]) * f.w);
+                    }
                     tc::tmem_st32(ta, o);
                 }
                 tc::tmem_wait_st();
@@ -787,7 +1067,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             const int cslot = slot;
             const uint32_t cpar = par0;
             if (c + 1 < n) {
-                if (!next_ready) {
+                if (!(ready & 1u)) {
                     (void)pm_wait(ctl, &ctl->kv_full[nslot], npar);
                     next = ctl->unit[nslot];
                 }
@@ -796,73 +1076,61 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             slot2 = slot1; par2 = par1;
             slot1 = slot; par1 = par0;
             slot = nslot; par0 = npar;
-            if (!(cur.flags & kUnitLast)) continue;
+            if (!cur.is(kUnitLast)) continue;
 
             // -------------------------------------------------------------- end of a part
-            // Every S of this part is done: the next row tile's queries are loaded while
-            // the last PV runs, and its products start behind this part's output.
+            // The last part is written by all warps, below. Behind any other, every S of
+            // the part is done: the next row tile's queries are loaded while the last PV
+            // runs, and its products start behind this part's output.
             const bool more = c + 1 < n;
             if (more) load_q(tile + 1);
             bad = !pm_wait(ctl, &ctl->kv_empty[cslot], cpar);   // the part's last PV
             if (owner) ctl->linv[hh] = l != 0.f ? out_scale / l : 0.f;
             if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
-            if (more) release_q();
-            tc::fence_after_sync();
             const int nr = rt.rows(tile);
             const size_t row0 = (size_t)rt.first_row(tile);
-            ++tile;
             if (cur.part < 0) {
                 if (lse && owner && hh < nr)
                     lse[row0 + hh] = l != 0.f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
-                // Lanes 2i and 2i+1 hold channels L, L+1: the even lane writes both
-                // channels of row j, the odd lane those of row j+1.
-                const bool odd = lane & 1;
-                __nv_bfloat16 *ob = out + row0 * kL;
-#pragma unroll 1
-                for (int blk = 0; blk < 8; ++blk) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(tl + (blk >> 1) * 64 + (blk & 1) * 32, o);
-                    tc::tmem_wait_ld();
-                    const int L2 = (blk >> 1) * 128 + 32 * wq + (lane & ~1);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float x = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? o[j] : o[j + 1]), 1);
-                        const float y = __uint_as_float(odd ? o[j + 1] : o[j]);
-                        const int r = (blk & 1) * 32 + j + (odd ? 1 : 0);
-                        const float inv = ctl->linv[r];
-                        // a row that saw nothing is 0 whatever its column holds
-                        const float lo = inv != 0.f ? (odd ? x : y) * inv : 0.f;
-                        const float hi = inv != 0.f ? (odd ? y : x) * inv : 0.f;
-                        if (r < nr) *reinterpret_cast<uint32_t *>(ob + (size_t)r * kL + L2) = pack_bf16x2(lo, hi);
-                    }
-                }
-            } else {
-                if (owner) part_ml[(size_t)cur.part * kPmRows + hh] = make_float2(m_used, l);
-                float *po = part + (size_t)cur.part * kPmRows * kL;
-#pragma unroll 1
-                for (int blk = 0; blk < 8; ++blk) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(tl + (blk >> 1) * 64 + (blk & 1) * 32, o);
-                    tc::tmem_wait_ld();
-                    const int L = (blk >> 1) * 128 + 32 * wq + lane;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int r = (blk & 1) * 32 + j;
-                        if (r < nr) po[(size_t)r * kL + L] = __uint_as_float(o[j]);
-                    }
-                }
+            } else if (owner) {
+                part_ml[(size_t)cur.part * kPmRows + hh] = make_float2(m_used, l);
             }
+            if (!more) {
+                if (tid == 0) {
+                    ctl->last_tile = tile;
+                    ctl->last_part = cur.part;
+                }
+                break;
+            }
+            release_q();
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int blk = 0; blk < 8; ++blk)
+                pm_write_rows(ctl, tl, wq, blk, nr, row0, cur.part, out, part);
             tc::fence_before_sync();
             tc::named_bar_sync(2, 128);       // linv is read before the next part writes it
+            ++tile;
             m_used = -INFINITY;
             l = 0.f;
         }
-        (void)failed;
+        if (failed && tid == 0) ctl->last_tile = -1;
         tc::cp_async_wait_all();
     }
 
-    // Every MMA of this CTA has completed before tensor memory is released.
     __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    // The last part out of tensor memory: warp w reads the lane quarter w % 4, three
+    // warps a quarter sharing its eight pieces.
+    const int tile = n > 0 ? ctl->last_tile : -1;
+    if (tile >= 0 && warp < 12) {
+#pragma unroll 1
+        for (int blk = warp >> 2; blk < 8; blk += 3)
+            pm_write_rows(ctl, tmem + ((uint32_t)(32 * (warp & 3)) << 16), warp & 3, blk, rt.rows(tile),
+                          (size_t)rt.first_row(tile), ctl->last_part, out, part);
+    }
+    // Every MMA of this CTA has completed, and every read, before tensor memory is released.
     if (warp == kPmIssuer) (void)mbar_wait(&ctl->fin, 0);
     tc::fence_before_sync();
     __syncthreads();
@@ -870,18 +1138,21 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     if (warp == kPmIssuer) tc::tmem_dealloc(tmem, 512);
 }
 
-// Row tiles that were split: entry blockIdx.x, kRowsPerBlock rows a block. 512
-// threads are four groups of 128 (4 channels a thread), each merging every
-// fourth part in order; the groups are merged in order (deterministic).
-constexpr int kMergeGroups = 4;
+// Row tiles that were split: entry blockIdx.x, rows_per_block rows and a quarter
+// of the channels a block. Its four warps merge every fourth part each, four
+// channels a lane and four parts in flight, then warp 0 merges the four in order
+// (deterministic). Blocks are small so that they wait beside the CTAs of
+// the split kernel and start with its end.
+constexpr int kMergeWarps = 4;
 
-__global__ void __launch_bounds__(kMergeGroups * 128)
+__global__ void __launch_bounds__(kMergeWarps * 32)
 prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict__ part_ml,
                         const MergeEntry *__restrict__ merge, int Q, int Hm, int rows_per_block,
                         float out_scale, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
-    __shared__ float4 so[kMergeGroups][128];
-    __shared__ float2 sml[kMergeGroups];
-    const int grp = threadIdx.x >> 7, ct = threadIdx.x & 127;
+    __shared__ float4 so[kMergeWarps][32];
+    __shared__ float2 sml[kMergeWarps];
+    const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c4 = blockIdx.z * 32 + lane;               // its four channels
     pdl_wait();
     pdl_launch_dependents();
     const MergeEntry e = merge[blockIdx.x];
@@ -895,15 +1166,15 @@ prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict
         float M = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int kU = 4;
-        for (int i0 = grp; i0 < e.parts; i0 += kU * kMergeGroups) {
+        for (int i0 = grp; i0 < e.parts; i0 += kU * kMergeWarps) {
             float2 ml[kU];
             float4 v[kU];
 #pragma unroll
             for (int k = 0; k < kU; ++k) {
-                const int i = i0 + k * kMergeGroups;
+                const int i = i0 + k * kMergeWarps;
                 const bool in = i < e.parts;
                 ml[k] = in ? part_ml[slot(i) * kPmRows + r] : make_float2(-INFINITY, 0.f);
-                v[k] = in ? reinterpret_cast<const float4 *>(part + (slot(i) * kPmRows + r) * kL)[ct]
+                v[k] = in ? reinterpret_cast<const float4 *>(part + (slot(i) * kPmRows + r) * kL)[c4]
                           : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float Mn = M;
@@ -923,21 +1194,21 @@ prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict
                 o.w = fmaf(v[k].w, wt, o.w);
             }
         }
-        so[grp][ct] = o;
-        if (ct == 0) sml[grp] = make_float2(M, l);
+        so[grp][lane] = o;
+        if (lane == 0) sml[grp] = make_float2(M, l);
         __syncthreads();
         if (grp == 0) {
             float Ma = M;
 #pragma unroll
-            for (int k = 1; k < kMergeGroups; ++k) Ma = fmaxf(Ma, sml[k].x);
+            for (int k = 1; k < kMergeWarps; ++k) Ma = fmaxf(Ma, sml[k].x);
             float lt = 0.f;
             float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kMergeGroups; ++k) {
+            for (int k = 0; k < kMergeWarps; ++k) {
                 const float2 ml = sml[k];
                 if (ml.y == 0.f) continue;
                 const float wt = ex2(ml.x - Ma);
-                const float4 v = so[k][ct];
+                const float4 v = so[k][lane];
                 lt = fmaf(ml.y, wt, lt);
                 t.x = fmaf(v.x, wt, t.x);
                 t.y = fmaf(v.y, wt, t.y);
@@ -948,8 +1219,8 @@ prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict
             uint2 pk;
             pk.x = pack_bf16x2(lt != 0.f ? t.x * inv : 0.f, lt != 0.f ? t.y * inv : 0.f);
             pk.y = pack_bf16x2(lt != 0.f ? t.z * inv : 0.f, lt != 0.f ? t.w * inv : 0.f);
-            *reinterpret_cast<uint2 *>(out + (size_t)(row0 + r) * kL + 4 * ct) = pk;
-            if (lse && ct == 0)
+            *reinterpret_cast<uint2 *>(out + (size_t)(row0 + r) * kL + 4 * c4) = pk;
+            if (lse && c4 == 0)
                 lse[row0 + r] = lt != 0.f ? (Ma + log2f(lt)) * 0.6931471805599453f : -INFINITY;
         }
         __syncthreads();
@@ -978,14 +1249,14 @@ inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, in
             return DSA_ERR_CUDA;
     }
     if (!ensure_smem_attr(reinterpret_cast<const void *>(prefix_mla_kernel<kFp8, kWidth>),
-                          PmSmem<kWidth>::kBytes))
+                          PmSmem<kFp8, kWidth>::kBytes))
         return DSA_ERR_CUDA;
     auto *part = reinterpret_cast<float *>(ws);
     auto *ml = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(ws) + kPmPartBytes);
     auto *merge = reinterpret_cast<MergeEntry *>(reinterpret_cast<uint8_t *>(ws) + kPmPartBytes + kPmMlBytes);
     auto *ob = reinterpret_cast<__nv_bfloat16 *>(out);
     if (launch_pdl(prefix_mla_kernel<kFp8, kWidth>, dim3(kPmGrid), dim3(kPmThreads),
-                   PmSmem<kWidth>::kBytes, stream, map, box_rows,
+                   PmSmem<kFp8, kWidth>::kBytes, stream, map, box_rows,
                    reinterpret_cast<const __nv_bfloat16 *>(q), kv, g, Hm, scale_log2, out_scale, part,
                    ml, merge, ob, lse) != cudaSuccess)
         return DSA_ERR_CUDA;
@@ -996,8 +1267,8 @@ inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, in
     const RowTiles rt(g.Q, Hm);
     const bool by_tile = rt.count <= kPmGrid;
     const int rpb = by_tile ? 1 : 8;
-    if (launch_pdl(prefix_mla_merge_kernel, dim3(by_tile ? rt.count : kPmGrid, kPmRows / rpb),
-                   dim3(kMergeGroups * 128), 0, stream, part, ml, merge, g.Q, Hm, rpb, out_scale, ob,
+    if (launch_pdl(prefix_mla_merge_kernel, dim3(by_tile ? rt.count : kPmGrid, kPmRows / rpb, kL / 128),
+                   dim3(kMergeWarps * 32), 0, stream, part, ml, merge, g.Q, Hm, rpb, out_scale, ob,
                    lse) != cudaSuccess)
         return DSA_ERR_CUDA;
     return launch_status();
@@ -1029,6 +1300,9 @@ inline int prefix_mla_launch(const void *q, const void *kv, float kv_scale, int6
         return DSA_ERR_ALIGNMENT;
     if (!ws || ws_bytes < prefix_mla_workspace_bytes(g.Q, Hm)) return DSA_ERR_WORKSPACE;
     g.kv_rows = (int)kv_rows;
+    g.page_shift = -1;
+    if ((g.page & (g.page - 1)) == 0)
+        for (g.page_shift = 0; (1 << g.page_shift) < g.page;) ++g.page_shift;
     const float scale_log2 = (kFp8 ? sm_scale * kv_scale : sm_scale) * 1.4426950408889634f;
     const float out_scale = kFp8 ? kv_scale : 1.0f;
     return rope ? prefix_mla_run<kFp8, DSA_KV_LORA + kRopeDim>(q, kv, g, Hm, scale_log2, out_scale,

@@ -249,3 +249,21 @@ def test_equals_the_sparse_call_on_every_token(lib):
     tol = 2.0 ** -8 * np.abs(ref) + (2 * 2.0 ** -8 + 2.0 ** -12) * mag
     assert (np.abs(out.float().cpu().numpy() - ref) <= tol).all()
     assert np.abs(lse.cpu().numpy() - o["lse"].cpu().numpy()).max() < 1e-4
+
+
+def test_every_fp8_code(lib):
+    # rows of all 256 codes, NaN codes among them: values are exact, and a NaN shows where it lies
+    for rope in (0, 64):
+        b = Batch(23, [40, 64], prefix=0, page=32, hm=16, rope=rope, fp8=True, fill=0.0, scale=0.5)
+        rng = np.random.default_rng(1)
+        b.codes[:] = rng.integers(0, 256, b.codes.shape)
+        b.codes[(b.codes & 0x7F) == 0x7F] = 0x80
+        b.values = O.e4m3_to_f64(b.codes) * 0.5
+        b.q *= np.float32(2.0 ** -6)                  # codes reach 448
+        d, o = b.run_and_check(lib)
+        row = O.paged_row(b.table[0], 32, 5, b.rows)
+        d["cache"][row, 77], d["cache"][row, 300] = 0x7F, 0xFF
+        b.call(lib, d, o)
+        torch.cuda.synchronize()
+        out = o["out"].float()
+        assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
