@@ -52,7 +52,7 @@ struct PrefixGeom {
 constexpr int kPmTile = 32;                           // tokens of a unit: one S product
 constexpr int kPmRows = 64;                           // (query, head) rows of a row tile
 constexpr int kPmGrid = 148;                          // persistent CTAs, one per SM
-constexpr int kPmMinUnits = 4;                        // units a CTA takes at least
+constexpr int kPmMinUnits = 2;                        // units a CTA takes at least
 constexpr int kPmPartUnits = 5;                       // units that a further part of a CTA costs
 constexpr int kPmThreads = 512;                       // 4 softmax warps, 8 loaders, S and PV issuers, 2 fetchers
 constexpr int kPmIssuer = 12;
@@ -192,7 +192,9 @@ static_assert(PmSmem<false, 576>::kBytes <= 232448 && PmSmem<false, 512>::kBytes
                   PmSmem<true, 576>::kBytes <= 232448 && PmSmem<true, 512>::kBytes <= 232448,
               "shared memory per block");
 static_assert(PmSmem<false, 512>::kSlots <= kPmMaxSlots, "ring");
-static_assert(65535 * 2 <= (int)(kPmPBytes / 8) * kPmThreads, "block sums hold every row tile");
+constexpr int kPmScratch = kPmGrid * (int)(sizeof(int) + sizeof(TileWalk));
+static_assert(65535 * 2 <= kPmScratch / 8 * kPmThreads, "block sums hold every row tile");
+static_assert(kPmScratch <= 3 * PmSmem<true, 512>::kSlot, "the plan's scratch");
 
 // Bounded wait of a warp that may sleep: the hint lets the hardware hold the warp
 // until the phase completes instead of answering "not yet" at once, since a dozen
@@ -277,7 +279,7 @@ DSA_DEVINL long long warp_inclusive_sum(long long v, int lane) {
 // then leaves at most two, one of its first and one of its last row tile. Where
 // there are fewer row tiles than CTAs, whole CTAs are given to each instead if
 // the longest range grows by less than a second part costs (its queries, its
-// output: kPmPartUnits). scratch: shared, 8 KB.
+// output: kPmPartUnits). scratch: shared, kPmScratch bytes of the ring's.
 DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const RowTiles &rt, int P) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kPmThreads / 32;
@@ -292,7 +294,10 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
             w.load(g, rt, tid, P);
             units = w.units;
         }
-        if (tid < kPmGrid) reinterpret_cast<int *>(scratch)[tid] = units;
+        if (tid < kPmGrid) {
+            reinterpret_cast<int *>(scratch)[tid] = units;
+            if (tid < rt.count) reinterpret_cast<TileWalk *>(reinterpret_cast<int *>(scratch) + kPmGrid)[tid] = w;
+        }
         inc = warp_inclusive_sum(units, lane);
         if (lane == 31) ctl->warp_sum[warp] = inc;
         if (tid == 0) ctl->count = ctl->parts = 0;
@@ -366,8 +371,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
                         const int t = lane * kEach + i, u = tile_units[t];
                         const int each = (u + need[i] - 1) / need[i];
                         ctl->first_tile = t;
-                        w.load(g, rt, t, P);
-                        ctl->first = w;
+                        ctl->first = reinterpret_cast<const TileWalk *>(tile_units + kPmGrid)[t];
                         ctl->first_unit = min(u, b * each);
                         ctl->first_units = u;
                         ctl->count = max(0, min(each, u - b * each));
@@ -376,6 +380,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
                     before += need[i];
                 }
             }
+            tc::fence_proxy_async_smem();             // the scratch becomes the ring
             __syncthreads();
             return;
         }
@@ -404,51 +409,70 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
             ctl->count = (int)min((long long)INT32_MAX, min(per, total - begin));
         }
     }
+    tc::fence_proxy_async_smem();                     // the scratch becomes the ring
     __syncthreads();
 }
 
 // One of the eight pieces (128-channel block blk / 2, 32-row half blk % 2) of O^T in a
-// lane quarter, out of tensor memory: normalised bf16 rows, or a part's fp32 rows.
+// lane quarter, out of tensor memory. A part's fp32 rows: lane l holds channel l of 32
+// rows, and 32 lanes write 128 bytes of a row. Normalised bf16 rows: the fragment shape
+// gives a thread two rows of one channel, the transposing store makes rows of 32 channels
+// of them in shared memory (2 KB at `stage`, 16-byte columns exclusive-or'ed with the
+// row pair), and 16-byte pieces go out: 12 accesses a piece where exchanging channels
+// between lanes took 40.
 DSA_DEVINL void pm_write_rows(const PmCtl *ctl, uint32_t tquarter, int quarter, int blk, int nr, size_t row0,
-                              int part_slot, __nv_bfloat16 *out, float *part) {
+                              int part_slot, uint32_t stage, __nv_bfloat16 *out, float *part) {
     const int lane = threadIdx.x & 31;
-    uint32_t o[32];
-    tc::tmem_ld32(tquarter + (blk >> 1) * 64 + (blk & 1) * 32, o);
-    tc::tmem_wait_ld();
-    const int L = (blk >> 1) * 128 + 32 * quarter + lane, r0 = (blk & 1) * 32;
+    const int r0 = (blk & 1) * 32, L = (blk >> 1) * 128 + 32 * quarter;
+    const uint32_t src = tquarter + (blk >> 1) * 64 + (blk & 1) * 32;
+    if (r0 >= nr) return;
     if (part_slot >= 0) {
-        float *po = part + ((size_t)part_slot * kPmRows + r0) * kL + L;
+        uint32_t o[32];
+        tc::tmem_ld32(src, o);
+        tc::tmem_wait_ld();
+        float *po = part + ((size_t)part_slot * kPmRows + r0) * kL + L + lane;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
             if (r0 + j < nr) po[(size_t)j * kL] = __uint_as_float(o[j]);
         return;
     }
-    // All factors are read before the first store, which the compiler must take for one
-    // that could change them. A row that saw nothing is 0 whatever its column holds.
+    // Registers 4g .. 4g+3 of each half: channels lane/4 and lane/4 + 8, rows
+    // 8g + 2 (lane%4) and the next.
+    uint32_t a[16], b[16];
+    tc::tmem_ld16x256b_x4(src, a);
+    tc::tmem_ld16x256b_x4(src + (16u << 16), b);
+    tc::tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(&ctl->linv[r0 + j]);
-        const float inv[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[j + k] = inv[k] != 0.f ? __float_as_uint(__uint_as_float(o[j + k]) * inv[k]) : 0u;
+    for (int g = 0; g < 4; ++g) {
+        const float2 f = *reinterpret_cast<const float2 *>(&ctl->linv[r0 + 8 * g + 2 * (lane & 3)]);
+        // a row that saw nothing is 0 whatever its column holds
+        auto pack = [&](uint32_t x, uint32_t y) {
+            return pack_bf16x2(f.x != 0.f ? __uint_as_float(x) * f.x : 0.f,
+                               f.y != 0.f ? __uint_as_float(y) * f.y : 0.f);
+        };
+        const int r = 8 * g + (lane & 7);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         stage + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4)),
+                     "r"(pack(a[4 * g], a[4 * g + 1])), "r"(pack(a[4 * g + 2], a[4 * g + 3])),
+                     "r"(pack(b[4 * g], b[4 * g + 1])), "r"(pack(b[4 * g + 2], b[4 * g + 3]))
+                     : "memory");
     }
-    // Lanes 2i and 2i+1 hold channels L, L+1: the even lane writes both channels of
-    // row j, the odd lane those of row j+1. Exchanges first, then stores: an exchange
-    // is not moved before a store, and would wait out its latency sixteen times.
-    const bool odd = lane & 1;
-    uint32_t v[16];
+    __syncwarp();
+    uint4 v[4];
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-        const float x = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? o[j] : o[j + 1], 1));
-        const float y = __uint_as_float(odd ? o[j + 1] : o[j]);
-        v[j / 2] = odd ? pack_bf16x2(x, y) : pack_bf16x2(y, x);
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                     : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4))
+                     : "memory");
     }
-    const int first = r0 + (odd ? 1 : 0);
-    __nv_bfloat16 *ob = out + (row0 + first) * kL + (L & ~1);
 #pragma unroll
-    for (int j = 0; j < 32; j += 2)
-        if (first + j < nr) *reinterpret_cast<uint32_t *>(ob + (size_t)j * kL) = v[j / 2];
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 8 * i + (lane >> 2);
+        if (r < nr) *reinterpret_cast<uint4 *>(out + (row0 + r) * kL + L + 8 * (lane & 3)) = v[i];
+    }
+    __syncwarp();                                     // the next piece takes the same stage
 }
 
 // kv: kv_rows rows of kWidth bf16, or E4M3 bytes (kFp8; widened to bf16, which
@@ -504,11 +528,22 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+    // Page tables and queries towards L2, each CTA its share, while the plan is worked out
+    // (a hint reads nothing: what a predecessor still writes is written to L2).
+    {
+        const long long at = ((long long)tid * gridDim.x + blockIdx.x) * 128;
+        const long long q_bytes = (long long)rt.total_rows * kWidth * 2;
+        if (at < q_bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(q) + at));
+        if (at < (long long)g.B * g.max_blocks * 4)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(g.block_table) + at));
+        if (at < (long long)g.prefix_blocks * 4)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(g.prefix_table) + at));
+    }
     pdl_wait();                       // queries, lengths and cache rows may come from the predecessor
     pdl_launch_dependents();
 
     const int P = g.shared_len();
-    pm_plan(ctl, gbase + S::kP, g, rt, P);
+    pm_plan(ctl, gbase + S::kKV, g, rt, P);
     const int n = ctl->count;
     const bool by_tile = rt.count <= kPmGrid;
     if (!by_tile && tid == 0) {
@@ -906,11 +941,6 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 else
                     tc::st_shared_zero16(dst);
             }
-            // All rows are asked for at once; the batches below then wait for L2 and not
-            // three times for memory.
-            for (int x = wtid; x < nr * (kPmQChannels / 64); x += 128)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (size_t)(row0 + x / (kPmQChannels / 64)) * kWidth +
-                                                              x % (kPmQChannels / 64) * 64));
             const uint4 *src = reinterpret_cast<const uint4 *>(q + (size_t)(row0 + min(hh, nr - 1)) * kWidth) + par;
             constexpr int kBatches = 3, kBatch = kPmQSteps * 8 / 32 / kBatches;   // 32-column blocks in flight
 #pragma unroll
@@ -1106,7 +1136,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             tc::fence_after_sync();
 #pragma unroll 1
             for (int blk = 0; blk < 8; ++blk)
-                pm_write_rows(ctl, tl, wq, blk, nr, row0, cur.part, out, part);
+                pm_write_rows(ctl, tl, wq, blk, nr, row0, cur.part, sP + wq * 2048, out, part);
             tc::fence_before_sync();
             tc::named_bar_sync(2, 128);       // linv is read before the next part writes it
             ++tile;
@@ -1128,7 +1158,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
 #pragma unroll 1
         for (int blk = warp >> 2; blk < 8; blk += 3)
             pm_write_rows(ctl, tmem + ((uint32_t)(32 * (warp & 3)) << 16), warp & 3, blk, rt.rows(tile),
-                          (size_t)rt.first_row(tile), ctl->last_part, out, part);
+                          (size_t)rt.first_row(tile), ctl->last_part, sKV + warp * 2048, out, part);
     }
     // Every MMA of this CTA has completed, and every read, before tensor memory is released.
     if (warp == kPmIssuer) (void)mbar_wait(&ctl->fin, 0);
