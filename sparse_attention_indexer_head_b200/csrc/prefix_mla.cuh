@@ -54,7 +54,9 @@ constexpr int kPmRows = 64;                           // (query, head) rows of a
 constexpr int kPmGrid = 148;                          // persistent CTAs, one per SM
 constexpr int kPmMinUnits = 2;                        // units a CTA takes at least
 constexpr int kPmPartUnits = 5;                       // units that a further part of a CTA costs
-constexpr int kPmThreads = 512;                       // 4 softmax warps, 8 loaders, S and PV issuers, 2 fetchers
+// Threads: 4 softmax warps, 8 loaders, the S and PV issuers, for E4M3 2 fetchers. (Without
+// those two, registers are left for the merge kernel's blocks to wait beside a CTA.)
+constexpr int pm_threads(bool fp8) { return fp8 ? 512 : 448; }
 constexpr int kPmIssuer = 12;
 constexpr int kPmQueries = 4;                         // queries a row tile holds at most
 
@@ -165,7 +167,7 @@ struct PmCtl {
     long long warp_sum[16];
     long long total, per, begin;
     int first_tile, first_unit, first_units, count, parts;
-    int candidate[16];
+    int whole_ctas;
     TileWalk first;                                   // of first_tile
     // The last part, written out by all warps.
     int last_tile, last_part;
@@ -193,7 +195,7 @@ static_assert(PmSmem<false, 576>::kBytes <= 232448 && PmSmem<false, 512>::kBytes
               "shared memory per block");
 static_assert(PmSmem<false, 512>::kSlots <= kPmMaxSlots, "ring");
 constexpr int kPmScratch = kPmGrid * (int)(sizeof(int) + sizeof(TileWalk));
-static_assert(65535 * 2 <= kPmScratch / 8 * kPmThreads, "block sums hold every row tile");
+static_assert(65535 * 2 <= kPmScratch / 8 * pm_threads(false), "block sums hold every row tile");
 static_assert(kPmScratch <= 3 * PmSmem<true, 512>::kSlot, "the plan's scratch");
 
 // Bounded wait of a warp that may sleep: the hint lets the hardware hold the warp
@@ -280,10 +282,11 @@ DSA_DEVINL long long warp_inclusive_sum(long long v, int lane) {
 // there are fewer row tiles than CTAs, whole CTAs are given to each instead if
 // the longest range grows by less than a second part costs (its queries, its
 // output: kPmPartUnits). scratch: shared, kPmScratch bytes of the ring's.
+template <int kThreads>
 DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const RowTiles &rt, int P) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kWarps = kPmThreads / 32;
-    const int nb = (rt.count + kPmThreads - 1) / kPmThreads;
+    constexpr int kWarps = kThreads / 32;
+    const int nb = (rt.count + kThreads - 1) / kThreads;
     const int G = (int)gridDim.x;
     TileWalk w;
     int units = 0;
@@ -300,7 +303,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
         }
         inc = warp_inclusive_sum(units, lane);
         if (lane == 31) ctl->warp_sum[warp] = inc;
-        if (tid == 0) ctl->count = ctl->parts = 0;
+        if (tid == 0) ctl->count = ctl->parts = ctl->whole_ctas = 0;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
@@ -309,11 +312,11 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
         }
     } else {
         auto *block_sum = reinterpret_cast<long long *>(scratch);
-        for (int k = tid; k < nb; k += kPmThreads) block_sum[k] = 0;
-        if (tid == 0) ctl->count = ctl->parts = 0;
+        for (int k = tid; k < nb; k += kThreads) block_sum[k] = 0;
+        if (tid == 0) ctl->count = ctl->parts = ctl->whole_ctas = 0;
         __syncthreads();
         for (int k = 0; k < nb; ++k) {
-            const int t = k * kPmThreads + tid;
+            const int t = k * kThreads + tid;
             units = 0;
             if (t < rt.count) {
                 w.load(g, rt, t, P);
@@ -337,49 +340,63 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
         ctl->per = per;
         ctl->begin = begin;
     }
-    if (rt.count > 1 && rt.count <= G && total < (1 << 30)) {
-        // Candidates for the longest range, one a warp, from `per` up to one that is
-        // sure to fit: total / hi + count <= G.
-        const auto *tile_units = reinterpret_cast<const int *>(scratch);
-        const int lo = (int)per;
-        const int hi = rt.count < G ? max(lo, ((int)total + G - rt.count - 1) / (G - rt.count)) : (int)total;
-        const int mine = lo + (int)((long long)(hi - lo) * warp / (kWarps - 1));
-        int ctas = 0;
-        for (int t = lane; t < rt.count; t += 32) ctas += (tile_units[t] + mine - 1) / mine;
-        ctas = __reduce_add_sync(0xffffffffu, ctas);
-        if (lane == 0) ctl->candidate[warp] = ctas <= G ? mine : INT32_MAX;
-        __syncthreads();
-        int best = INT32_MAX;
+    if (rt.count > 1 && rt.count <= G && total < (1 << 24)) {
+        // 1 + floor(units (G - count) / total) CTAs for a row tile: no more than G in all.
+        // By reciprocals, short of the quotient here and above it for the range a CTA takes.
+        if (warp == 0) {
+            const auto *tile_units = reinterpret_cast<const unsigned *>(scratch);
+            const float share = (float)(G - rt.count) * rcp_approx((float)total) * (1.f - 0x1p-20f);
+            // lane l: consecutive row tiles, up to five; their CTAs and longest range
+            constexpr int kEach = (kPmGrid + 31) / 32;
+            const int lane_tiles = (rt.count + 31) / 32;
+            unsigned need[kEach], each[kEach], sum = 0, longest = 0;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) best = min(best, ctl->candidate[k]);
-        if (best - lo < kPmPartUnits) {
-            if (warp == 0) {
-                // lane l: five consecutive row tiles; the CTAs before and in each
-                constexpr int kEach = (kPmGrid + 31) / 32;
-                int need[kEach], sum = 0;
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const int t = lane * kEach + i;
-                    need[i] = t < rt.count ? (tile_units[t] + best - 1) / best : 0;
-                    sum += need[i];
+            for (int i = 0; i < kEach; ++i) {
+                need[i] = each[i] = 0;
+                const int t = lane * lane_tiles + i;
+                if (i < lane_tiles && t < rt.count) {
+                    const unsigned u = tile_units[t];
+                    need[i] = 1u + (unsigned)((float)u * share);
+                    each[i] = (unsigned)((float)u * rcp_approx((float)need[i]) * (1.f + 0x1p-20f)) + 1u;
+                    each[i] = max(each[i], (unsigned)kPmMinUnits);
+                    if (need[i] == 1u) each[i] = u;
                 }
-                int before = (int)warp_inclusive_sum(sum, lane) - sum;
+                sum += need[i];
+                longest = max(longest, each[i]);
+            }
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            if (longest < (unsigned)per + kPmPartUnits) {
+                unsigned before = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned v = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += v;
+                }
+                before -= sum;
 #pragma unroll
                 for (int i = 0; i < kEach; ++i) {
-                    const int b = (int)blockIdx.x - before;
-                    if (b >= 0 && b < need[i]) {
-                        const int t = lane * kEach + i, u = tile_units[t];
-                        const int each = (u + need[i] - 1) / need[i];
+                    const unsigned k = blockIdx.x - before;
+                    if (k < need[i]) {
+                        const int t = lane * lane_tiles + i;
+                        const unsigned u = tile_units[t];
+                        unsigned parts = (unsigned)((float)u * rcp_approx((float)each[i]));
+                        while (parts * each[i] < u) ++parts;
+                        while (parts > 1 && (parts - 1) * each[i] >= u) --parts;
                         ctl->first_tile = t;
                         ctl->first = reinterpret_cast<const TileWalk *>(tile_units + kPmGrid)[t];
-                        ctl->first_unit = min(u, b * each);
-                        ctl->first_units = u;
-                        ctl->count = max(0, min(each, u - b * each));
-                        ctl->parts = (u + each - 1) / each;
+                        ctl->first_unit = (int)min(u, k * each[i]);
+                        ctl->first_units = (int)u;
+                        ctl->count = (int)(u - min(u, k * each[i]));
+                        ctl->count = min(ctl->count, (int)each[i]);
+                        ctl->parts = (int)parts;
                     }
                     before += need[i];
                 }
+                if (lane == 0) ctl->whole_ctas = 1;
             }
+        }
+        __syncthreads();
+        if (ctl->whole_ctas) {
             tc::fence_proxy_async_smem();             // the scratch becomes the ring
             __syncthreads();
             return;
@@ -389,7 +406,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
         if (nb > 1) {
             const auto *block_sum = reinterpret_cast<const long long *>(scratch);
             while (base + block_sum[kb] <= begin) base += block_sum[kb++];
-            const int t = kb * kPmThreads + tid;
+            const int t = kb * kThreads + tid;
             units = 0;
             if (t < rt.count) {
                 w.load(g, rt, t, P);
@@ -402,7 +419,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
         }
         const long long first = base + inc - units;
         if (units > 0 && first <= begin && begin < first + units) {
-            ctl->first_tile = kb * kPmThreads + tid;
+            ctl->first_tile = kb * kThreads + tid;
             ctl->first = w;
             ctl->first_unit = (int)(begin - first);
             ctl->first_units = units;
@@ -478,7 +495,7 @@ DSA_DEVINL void pm_write_rows(const PmCtl *ctl, uint32_t tquarter, int quarter, 
 // kv: kv_rows rows of kWidth bf16, or E4M3 bytes (kFp8; widened to bf16, which
 // is exact). box_rows: rows of a box of kv_map, 0 where pages allow none.
 template <bool kFp8, int kWidth>
-__global__ void __launch_bounds__(kPmThreads, 1)
+__global__ void __launch_bounds__(pm_threads(kFp8), 1)
 prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                   const __nv_bfloat16 *__restrict__ q, const void *__restrict__ kv,
                   const PrefixGeom g, int Hm, float scale_log2, float out_scale,
@@ -543,7 +560,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     pdl_launch_dependents();
 
     const int P = g.shared_len();
-    pm_plan(ctl, gbase + S::kKV, g, rt, P);
+    pm_plan<pm_threads(kFp8)>(ctl, gbase + S::kKV, g, rt, P);
     const int n = ctl->count;
     const bool by_tile = rt.count <= kPmGrid;
     if (!by_tile && tid == 0) {
@@ -933,6 +950,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         auto load_q = [&](int tile) {
             const int row0 = rt.first_row(tile), nr = rt.rows(tile);
             constexpr int kPieces = S::kQAtoms * 8;
+#pragma unroll 2
             for (int x = wtid; x < kPmRows * kPieces; x += 128) {
                 const int r = x / kPieces, cc = x % kPieces;
                 const uint32_t dst = sQ + (cc >> 3) * (kPmRows * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
@@ -942,22 +960,24 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                     tc::st_shared_zero16(dst);
             }
             const uint4 *src = reinterpret_cast<const uint4 *>(q + (size_t)(row0 + min(hh, nr - 1)) * kWidth) + par;
-            constexpr int kBatches = 3, kBatch = kPmQSteps * 8 / 32 / kBatches;   // 32-column blocks in flight
+            // Batches of two 32-column blocks. (Two batches in flight spill, and the loop over
+            // the units then pays for it.)
+            constexpr int kBlocks = kPmQSteps * 8 / 32, kBatch = 2;
 #pragma unroll
-            for (int b0 = 0; b0 < kBatches; ++b0) {
-                uint4 v[kBatch][4];
+            for (int b0 = 0; b0 < kBlocks; b0 += kBatch) {
+                uint4 x[kBatch][4];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[b][i] = src[(b0 * kBatch + b) * 8 + 2 * i];
+                    for (int i = 0; i < 4; ++i) x[b][i] = src[(b0 + b) * 8 + 2 * i];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     uint32_t o[16];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         // columns 8i + 4 par .. + 3 of the block are here; keep those of parity par
-                        const uint32_t s0 = par ? v[b][i].x : v[b][i].y, s1 = par ? v[b][i].z : v[b][i].w;
-                        const uint32_t k0 = par ? v[b][i].y : v[b][i].x, k1 = par ? v[b][i].w : v[b][i].z;
+                        const uint32_t s0 = par ? x[b][i].x : x[b][i].y, s1 = par ? x[b][i].z : x[b][i].w;
+                        const uint32_t k0 = par ? x[b][i].y : x[b][i].x, k1 = par ? x[b][i].w : x[b][i].z;
                         const uint32_t g0 = __shfl_xor_sync(0xffffffffu, s0, 2);
                         const uint32_t g1 = __shfl_xor_sync(0xffffffffu, s1, 2);
                         // register j is column par + 2j
@@ -969,7 +989,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                     if (hh >= nr)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) o[j] = 0u;
-                    tc::tmem_st16x64b_x16(tl + kPmQCol + (uint32_t)((b0 * kBatch + b) * 32), o);
+                    tc::tmem_st16x64b_x16(tl + kPmQCol + (uint32_t)((b0 + b) * 32), o);
                 }
             }
             tc::tmem_wait_st();
@@ -1168,90 +1188,131 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     if (warp == kPmIssuer) tc::tmem_dealloc(tmem, 512);
 }
 
-// Row tiles that were split: entry blockIdx.x, rows_per_block rows and a quarter
-// of the channels a block. Its four warps merge every fourth part each, four
-// channels a lane and four parts in flight, then warp 0 merges the four in order
-// (deterministic). Blocks are small so that they wait beside the CTAs of
-// the split kernel and start with its end.
-constexpr int kMergeWarps = 4;
+// Row tiles that were split: entry blockIdx.x, rows_per_block rows a block. A warp
+// takes a quarter of the channels of a row (four a lane), eight parts in flight at
+// once, and of up to four parts those of two rows; the block's two halves take
+// alternate rows. With blocks for each quarter (gridDim.z 4: at most four row
+// tiles, so many parts) the eight warps share a row's parts and warp 0 merges the
+// eight sums. The order of the sums depends on the parts alone. Blocks cost
+// about 1 ns each even where nothing was split, so there are about a thousand.
+constexpr int kMergeWarps = 8;
 
-__global__ void __launch_bounds__(kMergeWarps * 32)
+// Running sums of a row's parts in this lane's four channels.
+struct MergeRow {
+    float M = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    template <int kN>
+    DSA_DEVINL void add(const float2 (&ml)[kN], const float4 (&v)[kN]) {
+        float Mn = M;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) Mn = fmaxf(Mn, ml[k].x);
+        if (l != 0.f) {
+            const float keep = ex2(M - Mn);
+            l *= keep; o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+        }
+        M = Mn;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            if (ml[k].y == 0.f) continue;             // a part without tokens: its row holds nothing
+            const float wt = ex2(ml[k].x - M);
+            l = fmaf(ml[k].y, wt, l);
+            o.x = fmaf(v[k].x, wt, o.x);
+            o.y = fmaf(v[k].y, wt, o.y);
+            o.z = fmaf(v[k].z, wt, o.z);
+            o.w = fmaf(v[k].w, wt, o.w);
+        }
+    }
+    DSA_DEVINL void write(size_t row, int c4, float out_scale, __nv_bfloat16 *out, float *lse) const {
+        const bool any = l != 0.f;
+        const float inv = any ? out_scale / l : 0.f;
+        *reinterpret_cast<uint2 *>(out + row * kL + 4 * c4) =
+            any ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv))
+                : make_uint2(0u, 0u);
+        if (lse && c4 == 0) lse[row] = any ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+};
+
+__global__ void __launch_bounds__(kMergeWarps * 32, 4)
 prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict__ part_ml,
                         const MergeEntry *__restrict__ merge, int Q, int Hm, int rows_per_block,
                         float out_scale, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
     __shared__ float4 so[kMergeWarps][32];
     __shared__ float2 sml[kMergeWarps];
-    const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c4 = blockIdx.z * 32 + lane;               // its four channels
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
     const MergeEntry e = merge[blockIdx.x];
     const RowTiles rt(Q, Hm);
     if (e.tile < 0 || e.tile >= rt.count || e.parts <= 1) return;
     if (e.first_cta < 0 || e.parts > kPmGrid || e.first_cta + e.parts > kPmGrid) return;
-    const int nr = rt.rows(e.tile), row0 = rt.first_row(e.tile);
-    const int r1 = min(nr, (int)(blockIdx.y + 1) * rows_per_block);
-    for (int r = blockIdx.y * rows_per_block; r < r1; ++r) {
-        auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * e.first_cta + 1 : 2 * (e.first_cta + i)); };
-        float M = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kU = 4;
-        for (int i0 = grp; i0 < e.parts; i0 += kU * kMergeWarps) {
-            float2 ml[kU];
-            float4 v[kU];
+    const size_t row0 = (size_t)rt.first_row(e.tile);
+    const int rb = blockIdx.y * rows_per_block, r1 = min(rt.rows(e.tile), rb + rows_per_block);
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * e.first_cta + 1 : 2 * (e.first_cta + i)); };
+    // parts i0, i0 + step, ... of row r
+    auto load = [&](int i0, int step, int r, int c4, auto &ml, auto &v) {
 #pragma unroll
-            for (int k = 0; k < kU; ++k) {
-                const int i = i0 + k * kMergeWarps;
-                const bool in = i < e.parts;
-                ml[k] = in ? part_ml[slot(i) * kPmRows + r] : make_float2(-INFINITY, 0.f);
-                v[k] = in ? reinterpret_cast<const float4 *>(part + (slot(i) * kPmRows + r) * kL)[c4]
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float Mn = M;
-#pragma unroll
-            for (int k = 0; k < kU; ++k) Mn = fmaxf(Mn, ml[k].x);
-            const float keep = l != 0.f ? ex2(M - Mn) : 0.f;
-            M = Mn;
-            if (l != 0.f) { l *= keep; o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep; }
-#pragma unroll
-            for (int k = 0; k < kU; ++k) {
-                if (ml[k].y == 0.f) continue;         // a part without tokens: its row holds nothing
-                const float wt = ex2(ml[k].x - M);
-                l = fmaf(ml[k].y, wt, l);
-                o.x = fmaf(v[k].x, wt, o.x);
-                o.y = fmaf(v[k].y, wt, o.y);
-                o.z = fmaf(v[k].z, wt, o.z);
-                o.w = fmaf(v[k].w, wt, o.w);
-            }
+        for (int k = 0; k < (int)(sizeof(ml) / sizeof(ml[0])); ++k) {
+            const int i = i0 + k * step;
+            const bool in = i < e.parts && r < r1;
+            ml[k] = in ? part_ml[slot(i) * kPmRows + r] : make_float2(-INFINITY, 0.f);
+            v[k] = in ? reinterpret_cast<const float4 *>(part + (slot(i) * kPmRows + r) * kL)[c4]
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        so[grp][lane] = o;
-        if (lane == 0) sml[grp] = make_float2(M, l);
-        __syncthreads();
-        if (grp == 0) {
-            float Ma = M;
+    };
+    if (gridDim.z == 1) {
+        const int c4 = (warp & 3) * 32 + lane, half = warp >> 2;
+        if (e.parts <= 4) {
+            for (int r = rb + half; r < r1; r += 4) {
+                float2 ml[2][4];
+                float4 v[2][4];
+                load(0, 1, r, c4, ml[0], v[0]);
+                load(0, 1, r + 2, c4, ml[1], v[1]);
 #pragma unroll
-            for (int k = 1; k < kMergeWarps; ++k) Ma = fmaxf(Ma, sml[k].x);
-            float lt = 0.f;
-            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int a = 0; a < 2; ++a) {
+                    if (r + 2 * a >= r1) break;
+                    MergeRow row;
+                    row.add(ml[a], v[a]);
+                    row.write(row0 + r + 2 * a, c4, out_scale, out, lse);
+                }
+            }
+            return;
+        }
+        for (int r = rb + half; r < r1; r += 2) {
+            MergeRow row;
+            for (int i0 = 0; i0 < e.parts; i0 += 8) {
+                float2 ml[8];
+                float4 v[8];
+                load(i0, 1, r, c4, ml, v);
+                row.add(ml, v);
+            }
+            row.write(row0 + r, c4, out_scale, out, lse);
+        }
+        return;
+    }
+    const int c4 = blockIdx.z * 32 + lane;               // its four channels
+    for (int r = rb; r < r1; ++r) {
+        MergeRow row;
+        for (int i0 = warp; i0 < e.parts; i0 += 8 * kMergeWarps) {
+            float2 ml[8];
+            float4 v[8];
+            load(i0, kMergeWarps, r, c4, ml, v);
+            row.add(ml, v);
+        }
+        so[warp][lane] = row.o;
+        if (lane == 0) sml[warp] = make_float2(row.M, row.l);
+        __syncthreads();
+        if (warp == 0) {
+            float2 ml[kMergeWarps];
+            float4 v[kMergeWarps];
 #pragma unroll
             for (int k = 0; k < kMergeWarps; ++k) {
-                const float2 ml = sml[k];
-                if (ml.y == 0.f) continue;
-                const float wt = ex2(ml.x - Ma);
-                const float4 v = so[k][lane];
-                lt = fmaf(ml.y, wt, lt);
-                t.x = fmaf(v.x, wt, t.x);
-                t.y = fmaf(v.y, wt, t.y);
-                t.z = fmaf(v.z, wt, t.z);
-                t.w = fmaf(v.w, wt, t.w);
+                ml[k] = sml[k];
+                v[k] = so[k][lane];
             }
-            const float inv = lt != 0.f ? out_scale / lt : 0.f;
-            uint2 pk;
-            pk.x = pack_bf16x2(lt != 0.f ? t.x * inv : 0.f, lt != 0.f ? t.y * inv : 0.f);
-            pk.y = pack_bf16x2(lt != 0.f ? t.z * inv : 0.f, lt != 0.f ? t.w * inv : 0.f);
-            *reinterpret_cast<uint2 *>(out + (size_t)(row0 + r) * kL + 4 * c4) = pk;
-            if (lse && c4 == 0)
-                lse[row0 + r] = lt != 0.f ? (Ma + log2f(lt)) * 0.6931471805599453f : -INFINITY;
+            MergeRow all;
+            all.add(ml, v);
+            all.write(row0 + r, c4, out_scale, out, lse);
         }
         __syncthreads();
     }
@@ -1285,19 +1346,20 @@ inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, in
     auto *ml = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(ws) + kPmPartBytes);
     auto *merge = reinterpret_cast<MergeEntry *>(reinterpret_cast<uint8_t *>(ws) + kPmPartBytes + kPmMlBytes);
     auto *ob = reinterpret_cast<__nv_bfloat16 *>(out);
-    if (launch_pdl(prefix_mla_kernel<kFp8, kWidth>, dim3(kPmGrid), dim3(kPmThreads),
+    if (launch_pdl(prefix_mla_kernel<kFp8, kWidth>, dim3(kPmGrid), dim3(pm_threads(kFp8)),
                    PmSmem<kFp8, kWidth>::kBytes, stream, map, box_rows,
                    reinterpret_cast<const __nv_bfloat16 *>(q), kv, g, Hm, scale_log2, out_scale, part,
                    ml, merge, ob, lse) != cudaSuccess)
         return DSA_ERR_CUDA;
     const int st = launch_status();
     if (st != DSA_OK) return st;
-    // Few row tiles are split into many parts: an entry a tile and a block a row.
-    // Many are split at most where a CTA's range ends: an entry a CTA, 8 rows a block.
+    // Up to as many row tiles as CTAs: an entry a tile. More are split at most where a
+    // CTA's range ends: an entry a CTA.
     const RowTiles rt(g.Q, Hm);
-    const bool by_tile = rt.count <= kPmGrid;
-    const int rpb = by_tile ? 1 : 8;
-    if (launch_pdl(prefix_mla_merge_kernel, dim3(by_tile ? rt.count : kPmGrid, kPmRows / rpb, kL / 128),
+    const int entries = std::min(rt.count, kPmGrid);
+    const bool quarters = rt.count <= 4;
+    const int rpb = quarters ? 1 : std::max(2, 2 * ceil_div((long long)entries * kPmRows, 2 * 1024));
+    if (launch_pdl(prefix_mla_merge_kernel, dim3(entries, ceil_div(kPmRows, rpb), quarters ? kL / 128 : 1),
                    dim3(kMergeWarps * 32), 0, stream, part, ml, merge, g.Q, Hm, rpb, out_scale, ob,
                    lse) != cudaSuccess)
         return DSA_ERR_CUDA;
