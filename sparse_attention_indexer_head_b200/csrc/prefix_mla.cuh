@@ -1191,9 +1191,9 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
 // Row tiles that were split: entry blockIdx.x, rows_per_block rows a block. A warp
 // takes a quarter of the channels of a row (four a lane), eight parts in flight at
 // once, and of up to four parts those of two rows; the block's two halves take
-// alternate rows. With blocks for each quarter (gridDim.z 4: at most four row
-// tiles, so many parts) the eight warps share a row's parts and warp 0 merges the
-// eight sums. The order of the sums depends on the parts alone. Blocks cost
+// alternate rows. With blocks for each quarter (gridDim.z 4: at most eight row
+// tiles, so many parts) the warps of a row, four or eight, share its parts, and the
+// first of them merges their sums. The order of the sums depends on the parts alone. Blocks cost
 // about 1 ns each even where nothing was split, so there are about a thousand.
 constexpr int kMergeWarps = 8;
 
@@ -1291,24 +1291,25 @@ prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict
         return;
     }
     const int c4 = blockIdx.z * 32 + lane;               // its four channels
-    for (int r = rb; r < r1; ++r) {
+    const int share = kMergeWarps / rows_per_block, mine = warp % share;
+    for (int r = rb + warp / share; r - warp / share < r1; r += kMergeWarps / share) {
         MergeRow row;
-        for (int i0 = warp; i0 < e.parts; i0 += 8 * kMergeWarps) {
+        for (int i0 = mine; i0 < e.parts; i0 += 8 * share) {
             float2 ml[8];
             float4 v[8];
-            load(i0, kMergeWarps, r, c4, ml, v);
+            load(i0, share, r, c4, ml, v);
             row.add(ml, v);
         }
         so[warp][lane] = row.o;
         if (lane == 0) sml[warp] = make_float2(row.M, row.l);
         __syncthreads();
-        if (warp == 0) {
+        if (mine == 0 && r < r1) {
             float2 ml[kMergeWarps];
             float4 v[kMergeWarps];
 #pragma unroll
             for (int k = 0; k < kMergeWarps; ++k) {
-                ml[k] = sml[k];
-                v[k] = so[k][lane];
+                ml[k] = k < share ? sml[(warp + k) % kMergeWarps] : make_float2(-INFINITY, 0.f);
+                v[k] = so[(warp + k) % kMergeWarps][lane];
             }
             MergeRow all;
             all.add(ml, v);
@@ -1357,8 +1358,8 @@ inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, in
     // CTA's range ends: an entry a CTA.
     const RowTiles rt(g.Q, Hm);
     const int entries = std::min(rt.count, kPmGrid);
-    const bool quarters = rt.count <= 4;
-    const int rpb = quarters ? 1 : std::max(2, 2 * ceil_div((long long)entries * kPmRows, 2 * 1024));
+    const bool quarters = rt.count <= 8;
+    const int rpb = quarters ? (rt.count <= 2 ? 1 : 2) : std::max(2, 2 * ceil_div((long long)entries * kPmRows, 2 * 1024));
     if (launch_pdl(prefix_mla_merge_kernel, dim3(entries, ceil_div(kPmRows, rpb), quarters ? kL / 128 : 1),
                    dim3(kMergeWarps * 32), 0, stream, part, ml, merge, g.Q, Hm, rpb, out_scale, ob,
                    lse) != cudaSuccess)
