@@ -77,19 +77,27 @@ struct RowTiles {
     }
 };
 
-// The tokens a row tile walks: one segment for the shared prefix (all rows),
-// then one for each of its queries (that query's rows). With one query there is
-// one segment, its whole sequence. A query that sees only a part of the prefix
-// makes the tile walk every query on its own. Units lie at multiples of 32
-// tokens, so a unit's rows are whole pages or parts of them.
+// The tokens a row tile walks, in segments: the shared prefix (all rows); then, for
+// queries of one request that follow one another, the whole units that all of them
+// see (their rows), and each query's rest (its rows). With one query there is one
+// segment, its whole sequence. A query that sees only a part of the prefix makes the
+// tile walk without that segment. Units lie at multiples of 32 tokens, so a unit's
+// rows are whole pages or parts of them.
 struct TileWalk {
     int nq, npre, units, active;
     bool shared;
     int vis[kPmQueries], req[kPmQueries];
+    int common[kPmQueries];           // tokens below which query k walks with its run (a multiple of 32)
+    int runs;                         // 4 bits a query: queries of the run that it begins, 0 where it begins none
 
-    DSA_DEVINL int query_units(int k, int P) const {
-        const int end = (int)(((unsigned)vis[k] + kPmTile - 1) / kPmTile);
-        return !shared ? end : vis[k] > P ? end - (int)((unsigned)P / kPmTile) : 0;
+    DSA_DEVINL int run(int k) const { return (runs >> (4 * k)) & 15; }
+    // Segment 2k: the common units of the run that begins with query k; 2k + 1: the rest of query k.
+    DSA_DEVINL int segment_units(int j, int P) const {
+        const int k = j >> 1;
+        const unsigned base = shared ? (unsigned)P : 0u, from = max(base, (unsigned)common[k]) / kPmTile;
+        if (!(j & 1)) return run(k) > 1 && (unsigned)common[k] > base ? (int)(from - base / kPmTile) : 0;
+        return (unsigned)vis[k] > max(base, (unsigned)common[k])
+                   ? (int)(((unsigned)vis[k] + kPmTile - 1) / kPmTile - from) : 0;
     }
     DSA_DEVINL void load(const PrefixGeom &g, const RowTiles &rt, int t, int P) {
         const int q0 = rt.first_query(t);
@@ -115,10 +123,23 @@ struct TileWalk {
         }
         shared = shared && active != 0;
         npre = shared ? (int)(((unsigned)P + kPmTile - 1) / kPmTile) : 0;
+        // runs of queries of one request that all see something
+        runs = 0;
+        int start = 0, len_run = 0, least = 0;
+#pragma unroll
+        for (int k = 0; k < kPmQueries; ++k) {
+            const bool joins = k > 0 && len_run > 0 && vis[k] > 0 && req[k] == req[k - 1];
+            least = joins ? min(least, vis[k]) : vis[k];
+            len_run = joins ? len_run + 1 : vis[k] > 0 ? 1 : 0;
+            start = joins ? start : k;
+            runs = (runs & ~(15 << (4 * start))) | (len_run << (4 * start));
+#pragma unroll
+            for (int i = 0; i < kPmQueries; ++i)
+                if (i <= k && i >= start) common[i] = len_run > 1 ? least / kPmTile * kPmTile : 0;
+        }
         units = npre;
 #pragma unroll
-        for (int k = 0; k < kPmQueries; ++k)
-            if (k < nq) units += query_units(k, P);
+        for (int j = 0; j < 2 * kPmQueries; ++j) units += segment_units(j, P);
         units = max(units, 1);                        // a tile without tokens still writes its rows
     }
 };
@@ -736,45 +757,55 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         if (n > 0) w = ctl->first;
         long long global_unit = ctl->begin;
         int left = n;                                     // units from the current one on
-        // The segment of the current unit: query seg (-1: the prefix), its tokens s0 .. s1-1,
-        // the unit's first token, the units from this one to the segment's end, whether the
-        // unit is the segment's first; and for the row lookups the request's table.
-        int seg = -1, s0 = 0, s1 = 0, tok0 = 0, seg_left = 0;
+        // The segment of the current unit (-1: the prefix), its tokens s0 .. s1-1, the unit's
+        // first token, the units from this one to the segment's end, whether the unit is the
+        // segment's first, the queries whose common units this part has had; and for the row
+        // lookups the request's table.
+        int seg = -1, s0 = 0, s1 = 0, tok0 = 0, seg_left = 0, met = 0;
         bool seg_first = false;
         uint32_t rows_word = 0;
         const int32_t *pages = nullptr;
-        // the unit `skip` units behind the start of segment k of the tile, or of a later one
-        auto enter_segment = [&](int k, int skip) {
-            for (;; ++k) {
-                int nu = k < 0 ? w.npre : 0;
+        // the unit `skip` units behind the start of segment j of the tile, or of a later one
+        auto enter_segment = [&](int j, int skip) {
+            for (;; ++j) {
+                int nu = j < 0 ? w.npre : 0;
 #pragma unroll
-                for (int i = 0; i < kPmQueries; ++i)
-                    if (k == i && i < w.nq) nu = w.query_units(i, P);
-                if (skip < nu || k >= w.nq) {
+                for (int i = 0; i < 2 * kPmQueries; ++i)
+                    if (j == i) nu = w.segment_units(i, P);
+                if (skip < nu || j >= 2 * kPmQueries) {
                     seg_left = nu - skip;
                     break;
                 }
                 skip -= nu;
             }
-            seg = k;
+            const int k = j >> 1;
+            const bool common = j >= 0 && !(j & 1);
+            seg = j;
             seg_first = skip == 0;
-            s0 = k >= 0 && w.shared ? P : 0;
-            s1 = k < 0 ? P : 0;
-            int b = 0;
+            s0 = j >= 0 && w.shared ? P : 0;
+            s1 = j < 0 ? P : 0;
+            int b = 0, run = 1;
 #pragma unroll
             for (int i = 0; i < kPmQueries; ++i)
-                if (k == i) { s1 = w.vis[i]; b = w.req[i]; }
+                if (j >= 0 && k == i) {
+                    s1 = common ? w.common[i] : w.vis[i];
+                    if (!common) s0 = max(s0, w.common[i]);
+                    b = w.req[i];
+                    run = common ? w.run(i) : 1;
+                }
+            if (common) met |= ((1 << run) - 1) << k;
             if (w.active == 0) { s1 = 0; b = 0; seg_left = 1; }   // no query sees a token: an empty unit
             pages = g.block_table + (size_t)b * g.max_blocks;
             tok0 = (int)((unsigned)s0 / kPmTile * kPmTile) + skip * kPmTile;
-            rows_word = (k < 0 || rt.qpt == 1 || w.active == 0 ? (uint32_t)kPmRows << 8
-                                                              : (uint32_t)(k * Hm) | ((uint32_t)Hm << 8)) |
+            rows_word = (j < 0 || rt.qpt == 1 || w.active == 0 ? (uint32_t)kPmRows << 8
+                                                              : (uint32_t)(k * Hm) | ((uint32_t)(run * Hm) << 8)) |
                         ((uint32_t)w.active << 24);
         };
         // describe the current unit; returns the row of this lane's token
         auto describe = [&](UnitInfo &info) -> int {
             const bool first = u == part_begin, last = left == 1 || u + 1 == w.units;
-            const bool fresh = first || (seg >= 0 && seg_first && !(w.shared && part_begin < w.npre));
+            const bool summed = (w.shared && part_begin < w.npre) || ((seg & 1) && ((met >> (seg >> 1)) & 1));
+            const bool fresh = first || (seg >= 0 && seg_first && !summed);
             info.word = rows_word | (first ? kUnitFirst : 0u) | (last ? kUnitLast : 0u) | (fresh ? kUnitFresh : 0u);
             // read on the last unit alone: a part that is the whole tile has no slot
             info.part = part_begin == 0 && u + 1 == w.units ? -1 : 2 * (int)blockIdx.x + (part_begin == 0 ? 1 : 0);
@@ -800,6 +831,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             if (u >= w.units) {
                 u = 0;
                 part_begin = 0;
+                met = 0;
                 w.load(g, rt, ++tile, P);
                 enter_tile();
                 enter_segment(w.npre > 0 ? -1 : 0, 0);

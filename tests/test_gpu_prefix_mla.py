@@ -267,3 +267,28 @@ def test_every_fp8_code(lib):
         torch.cuda.synchronize()
         out = o["out"].float()
         assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.parametrize("hm", [16, 32])
+@pytest.mark.parametrize("prefix", [0, 45])
+def test_several_queries_of_one_request_share_a_walk(lib, hm, prefix):
+    # runs of two to four queries, runs broken by a padding row or an empty query, equal
+    # positions, positions far apart, and a run that ends at a unit's border
+    q_req = [0, 0, 0, 1, 2, 2, -1, 2, 0, 1, 1, 1, 1, 3, 3, 2, 2, 2, 2, 2]
+    own = [300, 100, 64, 33]
+    pos = [299, 10, 150, 99, 63, 63, 5, 31, 32, 96, 97, 98, 99, -50, 20, 63, 62, 32, 31, 0]
+    b = Batch(hm, own, prefix=prefix, page=16, hm=hm, q_req=q_req, q_pos=[p + prefix for p in pos])
+    b.run_and_check(lib)
+
+
+def test_a_later_draft_tokens_nan_stays_with_it(lib):
+    # token 70 is seen by the second query alone
+    b = Batch(24, [71], page=16, hm=16, per=2)
+    clean = b.oracle()
+    b.values[O.paged_row(b.table[0], 16, 70, b.rows), 5] = np.nan
+    d, o = b.device(), b.buffers(lib)
+    b.call(lib, d, o)
+    torch.cuda.synchronize()
+    out, lse = o["out"].float().cpu().numpy(), o["lse"].cpu().numpy()
+    assert_attention_close(out[:1], lse[:1], [x[:1] for x in clean], b.width)
+    assert np.isnan(out[1]).all()
