@@ -341,3 +341,114 @@ class StreamedDecode:
 
     def kernels_per_step(self) -> int:
         return self.steps[0].kernels_per_step()
+
+
+class PrefixDecode:
+    """Dense MLA over a paged latent cache for a batch whose requests share a prefix.
+
+    Owns the cache (bf16, or E4M3 with one scale), the page tables and the lengths on the
+    device. ``fill_prefix`` appends the shared prefix's latent rows once; ``step`` appends
+    one new row a request (normalised, rotated at its position; dsa_latent_append_paged),
+    rotates the step's query heads in the same launch and attends over prefix and own
+    tokens (dsa_prefix_mla_decode_paged). With ``graph`` the two calls are captured at the
+    first step and replayed: the lengths are device data, and every page a request can
+    come to hold is in its table from the start.
+    """
+
+    def __init__(self, requests: int, heads: int, max_own: int, prefix_len: int, *,
+                 norm_w: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor] = None,
+                 interleaved: bool = True, page: int = 64, fp8: bool = False, kv_scale: float = 1.0,
+                 eps: float = 1e-6, sm_scale: float = KV_LORA ** -0.5, graph: bool = False,
+                 device: str = "cuda"):
+        self.device = torch.device(device)
+        self.requests, self.heads, self.page, self.prefix_len = requests, heads, page, prefix_len
+        self.rope = 0 if cos_sin is None else int(cos_sin.shape[1])
+        self.width = KV_LORA + self.rope
+        self.fp8, self.kv_scale, self.eps, self.sm_scale = fp8, kv_scale, eps, sm_scale
+        self.interleaved, self.graph = interleaved, graph
+        self.max_len = prefix_len + max_own
+        dev = dict(device=self.device)
+        self.norm_w = None if norm_w is None else norm_w.to(self.device, torch.bfloat16)
+        self.cos_sin = None if cos_sin is None else cos_sin.to(self.device, torch.float32).contiguous()
+        if self.cos_sin is not None and self.cos_sin.shape[0] < self.max_len:
+            raise ValueError("cos_sin has fewer positions than the sequences may come to hold")
+        # pages: the prefix's, then each request's own from the page that the prefix ends in
+        n_prefix, whole = -(-prefix_len // page), prefix_len // page
+        n_all = -(-self.max_len // page)
+        own = n_all - whole
+        pages = torch.arange(n_prefix + requests * own, dtype=torch.int32)
+        self.prefix_table = pages[:max(1, n_prefix)].contiguous().to(self.device)
+        table = torch.full((requests, max(1, n_all)), -1, dtype=torch.int32)
+        if own:
+            table[:, whole:] = pages[n_prefix:].view(requests, own)
+        self.block_table = table.to(self.device)
+        self.kv_rows = pages.numel() * page
+        self.cache = torch.zeros(self.kv_rows, self.width, dtype=torch.uint8 if fp8 else torch.bfloat16, **dev)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.prefix_tokens = torch.tensor([prefix_len], **i32)
+        self.seq_len = torch.full((requests,), prefix_len, **i32)
+        self.q_req = torch.arange(requests, **i32)
+        self.q_pos = self.seq_len - 1
+        self.kv_new = torch.zeros(requests, self.width, dtype=torch.bfloat16, **dev)
+        self.q = torch.zeros(requests, heads, self.width, dtype=torch.bfloat16, **dev)
+        self.out = torch.empty(requests, heads, KV_LORA, dtype=torch.bfloat16, **dev)
+        self.lse = torch.empty(requests, heads, dtype=torch.float32, **dev)
+        self.ws = torch.empty(max(16, B.dsa_prefix_mla_workspace_size(requests, heads)), dtype=torch.uint8, **dev)
+        self.tokens = 0                       # own tokens of every request so far
+        self._captured = None
+
+    def _append(self, kv_new, tok_req, tok_pos, table, n_req, q=None, stream=None):
+        cs, queries = self.cos_sin, ()
+        if q is not None and self.rope:       # rotated in place, behind the latent columns
+            queries = (q[..., KV_LORA:], q.stride(0), q.stride(1), self.heads, q)
+        shape = (kv_new.stride(0), self.norm_w, self.eps, cs, 0 if cs is None else cs.shape[0],
+                 int(self.interleaved), tok_req, tok_pos, kv_new.shape[0], KV_LORA, self.rope, table,
+                 n_req, table.shape[-1], self.page)
+        if self.fp8:
+            B.dsa_latent_append_paged_fp8(kv_new, *shape, self.cache, self.kv_scale, self.kv_rows, *queries,
+                                          stream=stream)
+        else:
+            B.dsa_latent_append_paged(kv_new, *shape, self.cache, self.kv_rows, *queries, stream=stream)
+
+    def fill_prefix(self, kv_new: torch.Tensor, stream=None) -> None:
+        """Append the prefix's rows: kv_new bf16 [prefix_len, 512 + rope], as projected."""
+        if tuple(kv_new.shape) != (self.prefix_len, self.width):
+            raise ValueError(f"kv_new is {tuple(kv_new.shape)}, not {(self.prefix_len, self.width)}")
+        pos = torch.arange(self.prefix_len, dtype=torch.int32, device=self.device)
+        self._append(kv_new, torch.zeros_like(pos), pos, self.prefix_table, 1, stream=stream)
+
+    def _calls(self, stream=None):
+        self._append(self.kv_new, self.q_req, self.q_pos, self.block_table, self.requests, self.q, stream)
+        where = (self.prefix_table, self.prefix_table.numel(), self.prefix_tokens, self.block_table,
+                 self.block_table.shape[1], self.page, self.seq_len, self.q_req, self.q_pos, self.requests,
+                 self.requests, self.heads, KV_LORA, self.rope, self.sm_scale, self.out, self.lse, self.ws,
+                 self.ws.numel(), stream)
+        if self.fp8:
+            B.dsa_prefix_mla_decode_paged_fp8(self.q, self.cache, self.kv_scale, self.kv_rows, *where)
+        else:
+            B.dsa_prefix_mla_decode_paged(self.q, self.cache, self.kv_rows, *where)
+
+    def step(self, kv_new: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
+        """One token a request: kv_new bf16 [requests, 512 + rope] as projected, q bf16 [requests,
+        heads, 512 + rope] with its last rope columns not yet rotated. Returns the output
+        [requests, heads, 512] (its buffer, overwritten by the next step)."""
+        if self.prefix_len + self.tokens >= self.max_len:
+            raise ValueError("the requests' pages are full")
+        self.kv_new.copy_(kv_new, non_blocking=True)
+        self.q.copy_(q, non_blocking=True)
+        self.seq_len += 1
+        self.q_pos += 1
+        self.tokens += 1
+        if not self.graph:
+            self._calls()
+        else:
+            if self._captured is None:
+                self._calls()                                  # sets kernel attributes eagerly
+                # the eager step rotated q in place: the replay below starts from the caller's
+                self.q.copy_(q, non_blocking=True)
+                torch.cuda.synchronize(self.device)
+                self._captured = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(self._captured):
+                    self._calls()
+            self._captured.replay()
+        return self.out

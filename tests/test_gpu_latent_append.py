@@ -314,3 +314,64 @@ def test_append_then_sparse_mla(lib, fp8):
         p /= p.sum(1, keepdims=True)
         tol = 2.0 ** -8 * np.abs(p @ k) + (2 * 2.0 ** -8 + 2.0 ** -12) * (p @ np.abs(k))
         assert (np.abs(out[i].float().cpu().numpy() - p @ k) <= tol).all()
+
+
+@pytest.mark.parametrize("fp8,rope,graph", [(False, 64, True), (True, 64, False), (False, 0, False), (True, 0, True)])
+def test_pipeline_prefix_decode(lib, fp8, rope, graph):
+    """pipeline.PrefixDecode: the prefix filled once, then steps, against the oracle end to end:
+    each step's output for the rows that the cache holds."""
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    rng = np.random.default_rng(rope + fp8)
+    R, hm, P, page, scale, width = 3, 32, 37, 16, 0.0625, 512 + rope
+    w = bf16_round(1 + 0.1 * rng.standard_normal(512))
+    cs = cos_sin_table(64, rope) if rope else None
+    dec = PrefixDecode(R, hm, 20, P, norm_w=torch.from_numpy(w), cos_sin=None if cs is None else torch.from_numpy(cs),
+                       page=page, fp8=fp8, kv_scale=scale if fp8 else 1.0, graph=graph, sm_scale=width ** -0.5)
+    x = bf16_round(rng.standard_normal((P, width)))
+    dec.fill_prefix(to_bf16(x))
+    prefix, table = dec.prefix_table.cpu().numpy(), dec.block_table.cpu().numpy()
+    rows, _ = O.latent_append(x, w, 1e-6, cs, True, np.zeros(P, int), np.arange(P), prefix[None], page, dec.kv_rows)
+
+    def stored():
+        c = dec.cache.cpu()
+        return O.e4m3_to_f64(c.numpy()) * scale if fp8 else c.float().numpy().astype(np.float64)
+
+    def check(rows):
+        kv = stored()
+        for r, y in rows.items():
+            half = np.maximum(HALF_E4M3 * np.abs(y), SUB_E4M3 * scale) if fp8 else HALF_BF16 * np.abs(y)
+            assert (np.abs(kv[r] - y) <= half * (1 + 2.0 ** -18) + 2.0 ** -17).all()
+        return kv
+
+    check(rows)
+    for t in range(3):
+        x = bf16_round(rng.standard_normal((R, width)))
+        q = bf16_round(rng.standard_normal((R, hm, width)))
+        out = dec.step(to_bf16(x), to_bf16(q)).float().cpu().numpy()
+        assert lib.dsa_device_status(reset=True) == 0
+        pos = np.full(R, P + t)
+        rows, heads = O.latent_append(x, w, 1e-6, cs, True, np.arange(R), pos, table, page, dec.kv_rows,
+                                      q[..., 512:] if rope else None)
+        assert len(rows) == R
+        kv = check(rows)
+        turned = dec.q.float().cpu().numpy()
+        np.testing.assert_array_equal(turned[..., :512], q[..., :512])
+        for i, y in heads.items():
+            # half a step, and 2^-22 of a pair's two terms, each below 10
+            assert (np.abs(turned[i, :, 512:] - y) <= HALF_BF16 * np.abs(y) * (1 + 2.0 ** -18) + 2.0 ** -17).all()
+        want = O.prefix_mla(turned, kv, prefix, P, table, page, pos + 1, np.arange(R), pos, width ** -0.5)
+        assert_attention_close(out, dec.lse.cpu().numpy(), want, width)
+
+
+def test_pipeline_prefix_decode_refuses(lib):
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    with pytest.raises(ValueError):
+        PrefixDecode(1, 16, 8, 60, norm_w=None, cos_sin=torch.zeros(64, 64))        # 68 positions
+    dec = PrefixDecode(1, 16, 1, 4, norm_w=None)
+    with pytest.raises(ValueError):
+        dec.fill_prefix(torch.zeros(3, 512, dtype=torch.bfloat16, device="cuda"))
+    dec.fill_prefix(torch.zeros(4, 512, dtype=torch.bfloat16, device="cuda"))
+    row = torch.zeros(1, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 16, 512, dtype=torch.bfloat16, device="cuda")
+    dec.step(*row)
+    with pytest.raises(ValueError):
+        dec.step(*row)
