@@ -1,14 +1,17 @@
-"""ctypes binding of libdsa.so (include/dsa.h), one Python function per C entry point.
+"""Binding of libdsa.so (include/dsa.h), one Python function per C entry point.
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels. Pointer arguments accept a torch tensor (its data_ptr()), an int
 address or None; ``stream`` accepts a torch.cuda.Stream, an int handle or None
-(torch's current stream). A non-OK status raises DsaError. There is no
-fallback: importing this module fails loudly when libdsa.so is missing.
+(torch's current stream). A non-OK status raises DsaError. The calls that launch
+go through the extension module _dsacall, the queries through ctypes (``lib``, which
+has every entry point). There is no fallback: importing this module fails loudly
+when libdsa.so or _dsacall.so is missing.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -94,16 +97,23 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+def _load_call():
+    path = os.path.join(HERE, "_dsacall.so")
+    if not os.path.exists(path):
+        raise ImportError(
+            f"_dsacall.so not found at {path}; build it with "
+            "`python -m sparse_attention_indexer_head_b200.build` (no fallback exists)")
+    spec = importlib.util.spec_from_file_location(__package__ + "._dsacall", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_call = _load_call()
 # Size of the library's own scratch for dsa_sparse_mla_decode_noalloc, as built.
 DSA_NOALLOC_SCRATCH_BYTES = int(lib.dsa_noalloc_scratch_bytes())
-
-
-def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
 
 
 _raw_stream = None          # device index -> its current stream's handle, once CUDA is up
@@ -145,7 +155,7 @@ def dsa_device_status(reset: bool = True) -> int:
 
 
 def dsa_selftest_bounded_wait(result, stream=None) -> None:
-    _check("dsa_selftest_bounded_wait", lib.dsa_selftest_bounded_wait(_ptr(result), _stream(stream)))
+    _check("dsa_selftest_bounded_wait", _call.dsa_selftest_bounded_wait(result, _stream(stream)))
 
 
 def dsa_head_gate_supported(M: int, K: int, N: int) -> bool:
@@ -153,68 +163,68 @@ def dsa_head_gate_supported(M: int, K: int, N: int) -> bool:
 
 
 def dsa_head_gate(hidden, w, out, M: int, K: int, N: int, stream=None) -> None:
-    _check("dsa_head_gate", lib.dsa_head_gate(_ptr(hidden), _ptr(w), _ptr(out), M, K, N,
+    _check("dsa_head_gate", _call.dsa_head_gate(hidden, w, out, M, K, N,
                                               _stream(stream)))
 
 
 def dsa_kpool_compress(k, gate, tok_valid, req_start, B: int, D: int, kpool: int, max_pools: int,
                        ape, ln_w, ln_b, eps: float, pool_keys, pool_idx, pool_valid, first_valid,
                        stream=None) -> None:
-    _check("dsa_kpool_compress", lib.dsa_kpool_compress(
-        _ptr(k), _ptr(gate), _ptr(tok_valid), _ptr(req_start), B, D, kpool, max_pools, _ptr(ape),
-        _ptr(ln_w), _ptr(ln_b), float(eps), _ptr(pool_keys), _ptr(pool_idx), _ptr(pool_valid),
-        _ptr(first_valid), _stream(stream)))
+    _check("dsa_kpool_compress", _call.dsa_kpool_compress(
+        k, gate, tok_valid, req_start, B, D, kpool, max_pools, ape,
+        ln_w, ln_b, eps, pool_keys, pool_idx, pool_valid,
+        first_valid, _stream(stream)))
 
 
 def dsa_indexer_store(k_new, gate_new, valid_new, tok_req, tok_pos, n: int, D: int, req_start,
                       B: int, k, gate, tok_valid, stream=None) -> None:
-    _check("dsa_indexer_store", lib.dsa_indexer_store(
-        _ptr(k_new), _ptr(gate_new), _ptr(valid_new), _ptr(tok_req), _ptr(tok_pos), n, D,
-        _ptr(req_start), B, _ptr(k), _ptr(gate), _ptr(tok_valid), _stream(stream)))
+    _check("dsa_indexer_store", _call.dsa_indexer_store(
+        k_new, gate_new, valid_new, tok_req, tok_pos, n, D,
+        req_start, B, k, gate, tok_valid, _stream(stream)))
 
 
 def dsa_kpool_compress_tokens(k, gate, tok_valid, req_start, B: int, D: int, kpool: int,
                               max_pools: int, ape, ln_w, ln_b, eps: float, tok_begin, tok_end,
                               pool_keys, pool_idx, pool_valid, first_valid, stream=None) -> None:
-    _check("dsa_kpool_compress_tokens", lib.dsa_kpool_compress_tokens(
-        _ptr(k), _ptr(gate), _ptr(tok_valid), _ptr(req_start), B, D, kpool, max_pools, _ptr(ape),
-        _ptr(ln_w), _ptr(ln_b), float(eps), _ptr(tok_begin), _ptr(tok_end), _ptr(pool_keys),
-        _ptr(pool_idx), _ptr(pool_valid), _ptr(first_valid), _stream(stream)))
+    _check("dsa_kpool_compress_tokens", _call.dsa_kpool_compress_tokens(
+        k, gate, tok_valid, req_start, B, D, kpool, max_pools, ape,
+        ln_w, ln_b, eps, tok_begin, tok_end, pool_keys,
+        pool_idx, pool_valid, first_valid, _stream(stream)))
 
 
 def dsa_index_scores(q_idx, gate_w, q_req, q_pos, Q: int, H: int, D: int, pool_keys, pool_valid,
                      first_valid, B: int, kpool: int, max_pools: int, scores, cand,
                      stream=None) -> None:
-    _check("dsa_index_scores", lib.dsa_index_scores(
-        _ptr(q_idx), _ptr(gate_w), _ptr(q_req), _ptr(q_pos), Q, H, D, _ptr(pool_keys),
-        _ptr(pool_valid), _ptr(first_valid), B, kpool, max_pools, _ptr(scores), _ptr(cand),
+    _check("dsa_index_scores", _call.dsa_index_scores(
+        q_idx, gate_w, q_req, q_pos, Q, H, D, pool_keys,
+        pool_valid, first_valid, B, kpool, max_pools, scores, cand,
         _stream(stream)))
 
 
 def dsa_topk_expand(scores, cand, pool_idx, q_req, Q: int, B: int, max_pools: int, kpool: int,
                     select_k: int, top_pools, token_ids, stream=None) -> None:
-    _check("dsa_topk_expand", lib.dsa_topk_expand(
-        _ptr(scores), _ptr(cand), _ptr(pool_idx), _ptr(q_req), Q, B, max_pools, kpool, select_k,
-        _ptr(top_pools), _ptr(token_ids), _stream(stream)))
+    _check("dsa_topk_expand", _call.dsa_topk_expand(
+        scores, cand, pool_idx, q_req, Q, B, max_pools, kpool, select_k,
+        top_pools, token_ids, _stream(stream)))
 
 
 def dsa_topk_expand_tail(scores, cand, pool_idx, q_req, q_pos, first_valid, tok_valid, req_start,
                          Q: int, B: int, max_pools: int, kpool: int, select_k: int, top_pools,
                          token_ids, stream=None) -> None:
-    _check("dsa_topk_expand_tail", lib.dsa_topk_expand_tail(
-        _ptr(scores), _ptr(cand), _ptr(pool_idx), _ptr(q_req), _ptr(q_pos), _ptr(first_valid),
-        _ptr(tok_valid), _ptr(req_start), Q, B, max_pools, kpool, select_k, _ptr(top_pools),
-        _ptr(token_ids), _stream(stream)))
+    _check("dsa_topk_expand_tail", _call.dsa_topk_expand_tail(
+        scores, cand, pool_idx, q_req, q_pos, first_valid,
+        tok_valid, req_start, Q, B, max_pools, kpool, select_k, top_pools,
+        token_ids, _stream(stream)))
 
 
 def dsa_indexer_select(hidden, w, K: int, q_idx, q_req, q_pos, Q: int, H: int, D: int, pool_keys,
                        pool_valid, first_valid, pool_idx, B: int, kpool: int, max_pools: int,
                        select_k: int, gate_w, scores, cand, top_pools, token_ids,
                        stream=None) -> None:
-    _check("dsa_indexer_select", lib.dsa_indexer_select(
-        _ptr(hidden), _ptr(w), K, _ptr(q_idx), _ptr(q_req), _ptr(q_pos), Q, H, D, _ptr(pool_keys),
-        _ptr(pool_valid), _ptr(first_valid), _ptr(pool_idx), B, kpool, max_pools, select_k,
-        _ptr(gate_w), _ptr(scores), _ptr(cand), _ptr(top_pools), _ptr(token_ids), _stream(stream)))
+    _check("dsa_indexer_select", _call.dsa_indexer_select(
+        hidden, w, K, q_idx, q_req, q_pos, Q, H, D, pool_keys,
+        pool_valid, first_valid, pool_idx, B, kpool, max_pools, select_k,
+        gate_w, scores, cand, top_pools, token_ids, _stream(stream)))
 
 
 def dsa_sparse_mla_workspace_size(Q: int, Hm: int, W: int) -> int:
@@ -228,9 +238,9 @@ def dsa_sparse_mla_launch_count(Q: int, Hm: int, W: int) -> int:
 def dsa_sparse_mla_decode(q, kv, kv_rows: int, req_start, q_req, token_ids, Q: int, B: int,
                           Hm: int, W: int, kv_lora: int, rope_dim: int, sm_scale: float, out, lse,
                           workspace, workspace_bytes: int, stream=None) -> None:
-    _check("dsa_sparse_mla_decode", lib.dsa_sparse_mla_decode(
-        _ptr(q), _ptr(kv), int(kv_rows), _ptr(req_start), _ptr(q_req), _ptr(token_ids), Q, B, Hm, W, kv_lora,
-        rope_dim, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes),
+    _check("dsa_sparse_mla_decode", _call.dsa_sparse_mla_decode(
+        q, kv, kv_rows, req_start, q_req, token_ids, Q, B, Hm, W, kv_lora,
+        rope_dim, sm_scale, out, lse, workspace, workspace_bytes,
         _stream(stream)))
 
 
@@ -239,19 +249,19 @@ def dsa_sparse_mla_decode_noalloc(q, kv, kv_rows: int, req_start, q_req, token_i
                                   sm_scale: float, out, lse, stream=None) -> None:
     """dsa_sparse_mla_decode for callers that cannot allocate: the split-KV scratch is the
     library's own static device area (see include/dsa.h)."""
-    _check("dsa_sparse_mla_decode_noalloc", lib.dsa_sparse_mla_decode_noalloc(
-        _ptr(q), _ptr(kv), int(kv_rows), _ptr(req_start), _ptr(q_req), _ptr(token_ids), Q, B, Hm, W, kv_lora,
-        rope_dim, float(sm_scale), _ptr(out), _ptr(lse), _stream(stream)))
+    _check("dsa_sparse_mla_decode_noalloc", _call.dsa_sparse_mla_decode_noalloc(
+        q, kv, kv_rows, req_start, q_req, token_ids, Q, B, Hm, W, kv_lora,
+        rope_dim, sm_scale, out, lse, _stream(stream)))
 
 
 def dsa_sparse_mla_decode_paged(q, kv, kv_rows: int, block_table, max_blocks: int, page_size: int,
                                 seq_len, q_req, token_ids, Q: int, B: int, Hm: int, W: int,
                                 kv_lora: int, rope_dim: int, sm_scale: float, out, lse, workspace,
                                 workspace_bytes: int, stream=None) -> None:
-    _check("dsa_sparse_mla_decode_paged", lib.dsa_sparse_mla_decode_paged(
-        _ptr(q), _ptr(kv), kv_rows, _ptr(block_table), max_blocks, page_size, _ptr(seq_len),
-        _ptr(q_req), _ptr(token_ids), Q, B, Hm, W, kv_lora, rope_dim, float(sm_scale), _ptr(out),
-        _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+    _check("dsa_sparse_mla_decode_paged", _call.dsa_sparse_mla_decode_paged(
+        q, kv, kv_rows, block_table, max_blocks, page_size, seq_len,
+        q_req, token_ids, Q, B, Hm, W, kv_lora, rope_dim, sm_scale, out,
+        lse, workspace, workspace_bytes, _stream(stream)))
 
 
 def dsa_sparse_mla_decode_paged_fp8(q, kv8, kv_scale: float, kv_rows: int, block_table,
@@ -259,10 +269,10 @@ def dsa_sparse_mla_decode_paged_fp8(q, kv8, kv_scale: float, kv_rows: int, block
                                     Q: int, B: int, Hm: int, W: int, kv_lora: int, rope_dim: int,
                                     sm_scale: float, out, lse, workspace, workspace_bytes: int,
                                     stream=None) -> None:
-    _check("dsa_sparse_mla_decode_paged_fp8", lib.dsa_sparse_mla_decode_paged_fp8(
-        _ptr(q), _ptr(kv8), float(kv_scale), kv_rows, _ptr(block_table), max_blocks, page_size,
-        _ptr(seq_len), _ptr(q_req), _ptr(token_ids), Q, B, Hm, W, kv_lora, rope_dim,
-        float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+    _check("dsa_sparse_mla_decode_paged_fp8", _call.dsa_sparse_mla_decode_paged_fp8(
+        q, kv8, kv_scale, kv_rows, block_table, max_blocks, page_size,
+        seq_len, q_req, token_ids, Q, B, Hm, W, kv_lora, rope_dim,
+        sm_scale, out, lse, workspace, workspace_bytes, _stream(stream)))
 
 
 def dsa_latent_append_paged(kv_new, kv_new_stride: int, norm_w, eps: float, cos_sin, max_pos: int,
@@ -270,11 +280,11 @@ def dsa_latent_append_paged(kv_new, kv_new_stride: int, norm_w, eps: float, cos_
                             block_table, B: int, max_blocks: int, page_size: int, kv, kv_rows: int,
                             q_rot=None, q_tok_stride: int = 0, q_head_stride: int = 0, Hm: int = 0,
                             q=None, stream=None) -> None:
-    _check("dsa_latent_append_paged", lib.dsa_latent_append_paged(
-        _ptr(kv_new), kv_new_stride, _ptr(norm_w), float(eps), _ptr(cos_sin), max_pos,
-        int(interleaved), _ptr(tok_req), _ptr(tok_pos), n, kv_lora, rope_dim, _ptr(block_table), B,
-        max_blocks, page_size, _ptr(kv), kv_rows, _ptr(q_rot), q_tok_stride, q_head_stride, Hm,
-        _ptr(q), _stream(stream)))
+    _check("dsa_latent_append_paged", _call.dsa_latent_append_paged(
+        kv_new, kv_new_stride, norm_w, eps, cos_sin, max_pos,
+        int(interleaved), tok_req, tok_pos, n, kv_lora, rope_dim, block_table, B,
+        max_blocks, page_size, kv, kv_rows, q_rot, q_tok_stride, q_head_stride, Hm,
+        q, _stream(stream)))
 
 
 def dsa_latent_append_paged_fp8(kv_new, kv_new_stride: int, norm_w, eps: float, cos_sin,
@@ -283,11 +293,11 @@ def dsa_latent_append_paged_fp8(kv_new, kv_new_stride: int, norm_w, eps: float, 
                                 page_size: int, kv8, kv_scale: float, kv_rows: int, q_rot=None,
                                 q_tok_stride: int = 0, q_head_stride: int = 0, Hm: int = 0, q=None,
                                 stream=None) -> None:
-    _check("dsa_latent_append_paged_fp8", lib.dsa_latent_append_paged_fp8(
-        _ptr(kv_new), kv_new_stride, _ptr(norm_w), float(eps), _ptr(cos_sin), max_pos,
-        int(interleaved), _ptr(tok_req), _ptr(tok_pos), n, kv_lora, rope_dim, _ptr(block_table), B,
-        max_blocks, page_size, _ptr(kv8), float(kv_scale), kv_rows, _ptr(q_rot), q_tok_stride,
-        q_head_stride, Hm, _ptr(q), _stream(stream)))
+    _check("dsa_latent_append_paged_fp8", _call.dsa_latent_append_paged_fp8(
+        kv_new, kv_new_stride, norm_w, eps, cos_sin, max_pos,
+        int(interleaved), tok_req, tok_pos, n, kv_lora, rope_dim, block_table, B,
+        max_blocks, page_size, kv8, kv_scale, kv_rows, q_rot, q_tok_stride,
+        q_head_stride, Hm, q, _stream(stream)))
 
 
 def dsa_prefix_mla_workspace_size(Q: int, Hm: int) -> int:
@@ -299,10 +309,10 @@ def dsa_prefix_mla_decode_paged(q, kv, kv_rows: int, prefix_table, prefix_blocks
                                 Q: int, B: int, Hm: int, kv_lora: int, rope_dim: int,
                                 sm_scale: float, out, lse, workspace, workspace_bytes: int,
                                 stream=None) -> None:
-    _check("dsa_prefix_mla_decode_paged", lib.dsa_prefix_mla_decode_paged(
-        _ptr(q), _ptr(kv), kv_rows, _ptr(prefix_table), prefix_blocks, _ptr(prefix_len),
-        _ptr(block_table), max_blocks, page_size, _ptr(seq_len), _ptr(q_req), _ptr(q_pos), Q, B, Hm,
-        kv_lora, rope_dim, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes,
+    _check("dsa_prefix_mla_decode_paged", _call.dsa_prefix_mla_decode_paged(
+        q, kv, kv_rows, prefix_table, prefix_blocks, prefix_len,
+        block_table, max_blocks, page_size, seq_len, q_req, q_pos, Q, B, Hm,
+        kv_lora, rope_dim, sm_scale, out, lse, workspace, workspace_bytes,
         _stream(stream)))
 
 
@@ -311,8 +321,8 @@ def dsa_prefix_mla_decode_paged_fp8(q, kv8, kv_scale: float, kv_rows: int, prefi
                                     page_size: int, seq_len, q_req, q_pos, Q: int, B: int, Hm: int,
                                     kv_lora: int, rope_dim: int, sm_scale: float, out, lse,
                                     workspace, workspace_bytes: int, stream=None) -> None:
-    _check("dsa_prefix_mla_decode_paged_fp8", lib.dsa_prefix_mla_decode_paged_fp8(
-        _ptr(q), _ptr(kv8), float(kv_scale), kv_rows, _ptr(prefix_table), prefix_blocks,
-        _ptr(prefix_len), _ptr(block_table), max_blocks, page_size, _ptr(seq_len), _ptr(q_req),
-        _ptr(q_pos), Q, B, Hm, kv_lora, rope_dim, float(sm_scale), _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace_bytes, _stream(stream)))
+    _check("dsa_prefix_mla_decode_paged_fp8", _call.dsa_prefix_mla_decode_paged_fp8(
+        q, kv8, kv_scale, kv_rows, prefix_table, prefix_blocks,
+        prefix_len, block_table, max_blocks, page_size, seq_len, q_req,
+        q_pos, Q, B, Hm, kv_lora, rope_dim, sm_scale, out, lse,
+        workspace, workspace_bytes, _stream(stream)))

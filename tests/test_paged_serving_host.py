@@ -138,3 +138,35 @@ def test_oracle_prefix_mla_closed_forms():
     # one token: its value, whatever the logits
     out, lse, *_ = O.prefix_mla(np.ones((1, 1, 512)), kv, [], 0, [[2]], 4, [1], [0], [0], 0.5)
     assert out[0, 0, 0] == 8 and lse[0, 0] == pytest.approx(4.0)
+
+
+def test_fast_calls_convert_like_the_declarations(B):
+    """The extension module's calls against the same refusals through ctypes."""
+    import torch
+    call, t = B._call, torch.zeros(64, dtype=torch.float32)
+    # None, an address and a tensor are pointers; the status comes back as it is
+    assert call.dsa_head_gate(None, None, None, 4, 4096, 16, None) == B.DSA_ERR_INVALID_ARG
+    assert call.dsa_head_gate(FAKE + 4, FAKE, t, 4, 4096, 16, 0) == B.DSA_ERR_ALIGNMENT
+    assert call.dsa_head_gate(t, t, t, 0, 4096, 16, None) == B.DSA_OK
+    args = [FAKE] * 4 + [2, 128, 9, 8, FAKE, FAKE, FAKE, 1e-5] + [FAKE] * 4 + [None]
+    assert call.dsa_kpool_compress(*args) == B.lib.dsa_kpool_compress(*args) == B.DSA_ERR_UNSUPPORTED
+    args[11] = float("nan")
+    assert call.dsa_kpool_compress(*args) == B.lib.dsa_kpool_compress(*args)
+    assert call.dsa_head_gate(FAKE, FAKE, FAKE, np.int64(4), np.int32(4094), 16, None) == B.DSA_ERR_UNSUPPORTED
+    with pytest.raises(TypeError):
+        call.dsa_head_gate(None, None, None, 4, 4096, 16)
+    with pytest.raises(TypeError):
+        call.dsa_head_gate(None, None, None, 4.5, 4096, 16, None)
+    with pytest.raises(AttributeError):
+        call.dsa_head_gate("text", None, None, 4, 4096, 16, None)
+    with pytest.raises(OverflowError):
+        call.dsa_head_gate(None, None, None, 1 << 31, 4096, 16, None)
+    with pytest.raises(OverflowError):
+        call.dsa_sparse_mla_decode(*[FAKE] * 2, 64, *[FAKE] * 3, 1, 1, 16, 48, 512, 0, 0.1, FAKE, None, FAKE, -1, None)
+
+
+def test_every_launching_entry_point_has_a_fast_call(B):
+    queries = {"dsa_status_string", "dsa_abi_version", "dsa_device_status", "dsa_head_gate_supported",
+               "dsa_sparse_mla_workspace_size", "dsa_sparse_mla_launch_count", "dsa_noalloc_scratch_bytes",
+               "dsa_prefix_mla_workspace_size"}
+    assert {n for n in dir(B._call) if n.startswith("dsa_")} == set(B.EXPORTS) - queries
