@@ -23,6 +23,7 @@
 namespace dsa {
 
 constexpr int kAppendWarps = 8;
+constexpr int kAppendBlocks = 5;                      // resident on an SM at least
 constexpr int kAppendHeads = 16;                      // query heads a warp rotates
 constexpr int kRopeDim = 64;                          // rotated channels, where there are any
 constexpr int kRopeHalf = kRopeDim / 2;
@@ -55,11 +56,11 @@ DSA_DEVINL uint16_t pack_e4m3x2(float lo, float hi) {
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kAppendWarps * 32)
-latent_append_kernel(const AppendArgs a, int parts) {
-    const int lane = threadIdx.x & 31;
-    const long long task = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-    const int i = (int)(task / parts), part = (int)(task % parts);
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks)
+latent_append_kernel(const AppendArgs a) {
+    // a warp a token; blockIdx.y 0: its row, p: its query heads 16 (p-1) .. + 15
+    const int lane = threadIdx.x & 31, part = blockIdx.y;
+    const long long i = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_launch_dependents();
     if (i >= a.n) return;
@@ -70,6 +71,11 @@ latent_append_kernel(const AppendArgs a, int parts) {
         const __nv_bfloat16 *src = a.x + (size_t)i * a.x_stride;
         const uint4 u0 = *reinterpret_cast<const uint4 *>(src + 8 * lane);
         const uint4 u1 = *reinterpret_cast<const uint4 *>(src + 256 + 8 * lane);
+        uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
+        if (a.norm_w) {
+            w0 = ldg_nc_v4(a.norm_w + 8 * lane);
+            w1 = ldg_nc_v4(a.norm_w + 256 + 8 * lane);
+        }
         float r0 = 0.f, r1 = 0.f;                    // the rotated pair of this lane
         if (a.rope) {
             const __nv_bfloat16 *pr = src + DSA_KV_LORA;
@@ -86,17 +92,18 @@ latent_append_kernel(const AppendArgs a, int parts) {
         unpack8(u0, reinterpret_cast<float(&)[8]>(y[0]));
         unpack8(u1, reinterpret_cast<float(&)[8]>(y[8]));
         if (a.norm_w) {
-            float w[16];
-            unpack8(ldg_nc_v4(a.norm_w + 8 * lane), reinterpret_cast<float(&)[8]>(w[0]));
-            unpack8(ldg_nc_v4(a.norm_w + 256 + 8 * lane), reinterpret_cast<float(&)[8]>(w[8]));
             float ss = 0.f;
 #pragma unroll
             for (int k = 0; k < 16; ++k) ss = fmaf(y[k], y[k], ss);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const float rstd = rsqrtf(ss * (1.0f / DSA_KV_LORA) + a.eps);
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] = y[k] * rstd * w[k];
+            for (int k = 0; k < 8; ++k) {
+                y[2 * k] = y[2 * k] * rstd * bf16lo(w[k]);
+                y[2 * k + 1] = y[2 * k + 1] * rstd * bf16hi(w[k]);
+            }
         }
         if (a.rope) {
             const float c = __ldg(a.cos_sin + (size_t)pos * kRopeDim + lane);
@@ -149,7 +156,6 @@ latent_append_kernel(const AppendArgs a, int parts) {
         return;
     }
     // ---- query heads 16 (part-1) .. + 15 of token i: eight lanes a head, 8 channels a lane
-    if (b < 0 || b >= a.B || pos < 0 || pos >= a.max_pos) return;
     const int j = lane & 7;
     const int h0 = (part - 1) * kAppendHeads + (lane >> 3);
     uint4 u[4];
@@ -160,6 +166,7 @@ latent_append_kernel(const AppendArgs a, int parts) {
                                                            (size_t)h * a.q_head_stride + 8 * j)
                         : make_uint4(0u, 0u, 0u, 0u);
     }
+    if (b < 0 || b >= a.B || pos < 0 || pos >= a.max_pos) return;
     const float *cs = a.cos_sin + (size_t)pos * kRopeDim;
     float out[8];
     if (a.interleaved) {
@@ -236,10 +243,8 @@ inline int latent_append_launch(AppendArgs a, float kv_scale, int kv_lora, cudaS
         return DSA_ERR_ALIGNMENT;
     a.inv_scale = kFp8 ? 1.0f / kv_scale : 1.0f;
     const int parts = 1 + (heads ? ceil_div(a.Hm, kAppendHeads) : 0);
-    const long long blocks = ((long long)a.n * parts + kAppendWarps - 1) / kAppendWarps;
-    if (blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-    if (launch_pdl(latent_append_kernel<kFp8>, dim3((unsigned)blocks), dim3(kAppendWarps * 32), 0,
-                   stream, a, parts) != cudaSuccess)
+    if (launch_pdl(latent_append_kernel<kFp8>, dim3(ceil_div(a.n, kAppendWarps), parts),
+                   dim3(kAppendWarps * 32), 0, stream, a) != cudaSuccess)
         return DSA_ERR_CUDA;
     return launch_status();
 }
