@@ -273,17 +273,20 @@ DSA_DEVINL bool elect_one() {
 }
 
 // Four E4M3 codes (low byte first) widened to bf16 pairs by integer moves and one
-// multiplication: exponent and mantissa shifted to bf16's places give the value
-// times 2^-120, subnormals included, and the product with 2^120 is exact. NaN codes
+// multiplication: exponent and mantissa at bf16's places give the value times 2^-120,
+// subnormals included, and the product with 2^120 is exact. A code in a 16-bit lane
+// times 16 has them there and its sign 4 bits low: 240 times the sign bit moves it
+// up. (Multiply-adds: shifts and logic would all fall on one pipe.) NaN codes
 // (S.1111.111) would become 480: the result has bit 7 of their bytes set (adding 1
 // to seven ones is the one sum that carries; other bits mean nothing).
 DSA_DEVINL uint32_t e4m3x4_to_bf16x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
-    const uint32_t mag = v & 0x7F7F7F7Fu;
-    const uint32_t x = (__byte_perm(v, 0, 0x1404) & 0x80008000u) | (__byte_perm(mag, 0, 0x4140) << 4);
-    const uint32_t y = (__byte_perm(v, 0, 0x3424) & 0x80008000u) | (__byte_perm(mag, 0, 0x4342) << 4);
+    const uint32_t a = __byte_perm(v, 0, 0x4140), b = __byte_perm(v, 0, 0x4342);   // codes in low bytes
+    uint32_t x, y;
+    asm("mad.lo.u32 %0, %1, 240, %2;" : "=r"(x) : "r"(a & 0x00800080u), "r"(a * 16u));
+    asm("mad.lo.u32 %0, %1, 240, %2;" : "=r"(y) : "r"(b & 0x00800080u), "r"(b * 16u));
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7B807B80u));
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7B807B80u));
-    return mag + 0x01010101u;
+    return (v & 0x7F7F7F7Fu) + 0x01010101u;
 }
 
 DSA_DEVINL long long warp_inclusive_sum(long long v, int lane) {
