@@ -289,10 +289,10 @@ DSA_DEVINL uint32_t e4m3x4_to_bf16x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
     return (v & 0x7F7F7F7Fu) + 0x01010101u;
 }
 
-DSA_DEVINL long long warp_inclusive_sum(long long v, int lane) {
+DSA_DEVINL unsigned warp_inclusive_sum(unsigned v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
     return v;
@@ -311,7 +311,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
     const int nb = (rt.count + kThreads - 1) / kThreads;
-    const int G = (int)gridDim.x;
+    constexpr int G = kPmGrid;
     TileWalk w;
     int units = 0;
     long long base = 0, total = 0, inc;
@@ -325,7 +325,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
             reinterpret_cast<int *>(scratch)[tid] = units;
             if (tid < rt.count) reinterpret_cast<TileWalk *>(reinterpret_cast<int *>(scratch) + kPmGrid)[tid] = w;
         }
-        inc = warp_inclusive_sum(units, lane);
+        inc = warp_inclusive_sum((unsigned)units, lane);   // of 32 tiles of at most 2^26 units
         if (lane == 31) ctl->warp_sum[warp] = inc;
         if (tid == 0) ctl->count = ctl->parts = ctl->whole_ctas = 0;
         __syncthreads();
@@ -390,13 +390,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
             }
             longest = __reduce_max_sync(0xffffffffu, longest);
             if (longest < (unsigned)per + kPmPartUnits) {
-                unsigned before = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned v = __shfl_up_sync(0xffffffffu, before, o);
-                    if (lane >= o) before += v;
-                }
-                before -= sum;
+                unsigned before = warp_inclusive_sum(sum, lane) - sum;
 #pragma unroll
                 for (int i = 0; i < kEach; ++i) {
                     const unsigned k = blockIdx.x - before;
@@ -436,7 +430,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
                 w.load(g, rt, t, P);
                 units = w.units;
             }
-            inc = warp_inclusive_sum(units, lane);
+            inc = warp_inclusive_sum((unsigned)units, lane);
             if (lane == 31) ctl->warp_sum[warp] = inc;
             __syncthreads();
             for (int k = 0; k < warp; ++k) base += ctl->warp_sum[k];
@@ -569,6 +563,8 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+    if (!kFp8 && box_rows > 0 && tid == 32)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kv_map)));
     // Page tables and queries towards L2, each CTA its share, while the plan is worked out
     // (a hint reads nothing: what a predecessor still writes is written to L2).
     {
@@ -770,6 +766,16 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         const int32_t *pages = nullptr;
         // the unit `skip` units behind the start of segment j of the tile, or of a later one
         auto enter_segment = [&](int j, int skip) {
+            if (rt.qpt == 1) {                            // one query: its whole sequence
+                seg = 1;
+                seg_first = skip == 0;
+                s1 = w.vis[0];
+                seg_left = w.units - skip;
+                tok0 = skip * kPmTile;
+                pages = g.block_table + (size_t)(w.active ? w.req[0] : 0) * g.max_blocks;
+                rows_word = ((uint32_t)kPmRows << 8) | ((uint32_t)w.active << 24);
+                return;
+            }
             for (;; ++j) {
                 int nu = j < 0 ? w.npre : 0;
 #pragma unroll
@@ -816,11 +822,11 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             return t >= s0 && t < s1 ? g.row(pages, t, P) : -1;
         };
         // merge entries by row tile, left by the CTA that begins it
-        auto enter_tile = [&]() {
+        auto enter_tile = [&](int t, long long begin, int units) {
             if (by_tile && grp == 0 && sub == 0 && lane == 0) {
                 const int parts = ctl->parts ? ctl->parts
-                                             : (int)((global_unit + w.units - 1) / ctl->per) - (int)blockIdx.x + 1;
-                merge[tile] = MergeEntry{tile, (int)blockIdx.x, parts, 0};
+                                             : (int)((begin + units - 1) / ctl->per) - (int)blockIdx.x + 1;
+                merge[t] = MergeEntry{t, (int)blockIdx.x, parts, 0};
             }
         };
         // one unit forward; false behind the last
@@ -836,7 +842,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 part_begin = 0;
                 met = 0;
                 w.load(g, rt, ++tile, P);
-                enter_tile();
+                enter_tile(tile, global_unit, w.units);
                 enter_segment(w.npre > 0 ? -1 : 0, 0);
             } else {
                 enter_segment(seg + 1, 0);
@@ -844,10 +850,8 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             return true;
         };
 
-        if (n > 0) {
-            if (u == 0) enter_tile();
-            enter_segment(w.npre > 0 ? -1 : 0, u);
-        }
+        if (n > 0) enter_segment(w.npre > 0 ? -1 : 0, u);
+        const bool begins = n > 0 && u == 0;              // its entry is written behind the first copies
         bool more = n > 0;
         if (grp == 1) more = more && advance();
         int slot = grp;
@@ -963,6 +967,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 if (more) row = describe(info);
             }
         }
+        if (begins) enter_tile(ctl->first_tile, ctl->begin, ctl->first_units);
         tc::cp_async_wait_all();          // nothing of this warp in flight past here
     } else if (warp < 4) {
         // ------------------------------------------------------------------ softmax (warps 0-3)
@@ -1268,7 +1273,7 @@ struct MergeRow {
     }
 };
 
-__global__ void __launch_bounds__(kMergeWarps * 32, 4)
+__global__ void __launch_bounds__(kMergeWarps * 32, 3)
 prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict__ part_ml,
                         const MergeEntry *__restrict__ merge, int Q, int Hm, int rows_per_block,
                         float out_scale, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
@@ -1326,8 +1331,10 @@ prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict
         return;
     }
     const int c4 = blockIdx.z * 32 + lane;               // its four channels
-    const int share = kMergeWarps / rows_per_block, mine = warp % share;
-    for (int r = rb + warp / share; r - warp / share < r1; r += kMergeWarps / share) {
+    const int share = rows_per_block == 1 ? kMergeWarps : kMergeWarps / 2, mine = warp & (share - 1);
+    const int side = rows_per_block == 1 ? 0 : warp >> 2;
+    for (int r0 = rb; r0 < r1; r0 += rows_per_block) {
+        const int r = r0 + side;
         MergeRow row;
         for (int i0 = mine; i0 < e.parts; i0 += 8 * share) {
             float2 ml[8];
@@ -1343,8 +1350,8 @@ prefix_mla_merge_kernel(const float *__restrict__ part, const float2 *__restrict
             float4 v[kMergeWarps];
 #pragma unroll
             for (int k = 0; k < kMergeWarps; ++k) {
-                ml[k] = k < share ? sml[(warp + k) % kMergeWarps] : make_float2(-INFINITY, 0.f);
-                v[k] = so[(warp + k) % kMergeWarps][lane];
+                ml[k] = k < share ? sml[(warp + k) & (kMergeWarps - 1)] : make_float2(-INFINITY, 0.f);
+                v[k] = so[(warp + k) & (kMergeWarps - 1)][lane];
             }
             MergeRow all;
             all.add(ml, v);
@@ -1395,7 +1402,7 @@ inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, in
     const int entries = std::min(rt.count, kPmGrid);
     const bool quarters = rt.count <= 8;
     const int rpb = quarters ? (rt.count <= 2 ? 1 : 2) : std::max(2, 2 * ceil_div((long long)entries * kPmRows, 2 * 1024));
-    if (launch_pdl(prefix_mla_merge_kernel, dim3(entries, ceil_div(kPmRows, rpb), quarters ? kL / 128 : 1),
+    if (launch_pdl(prefix_mla_merge_kernel, dim3(entries, ceil_div(std::min(kPmRows, rt.total_rows), rpb), quarters ? kL / 128 : 1),
                    dim3(kMergeWarps * 32), 0, stream, part, ml, merge, g.Q, Hm, rpb, out_scale, ob,
                    lse) != cudaSuccess)
         return DSA_ERR_CUDA;

@@ -292,3 +292,23 @@ def test_a_later_draft_tokens_nan_stays_with_it(lib):
     out, lse = o["out"].float().cpu().numpy(), o["lse"].cpu().numpy()
     assert_attention_close(out[:1], lse[:1], [x[:1] for x in clean], b.width)
     assert np.isnan(out[1]).all()
+
+
+@pytest.mark.parametrize("requests,hm,lo,hi", [
+    (40, 64, 1100, 1900),      # fewer row tiles than CTAs, ranges that cross tiles
+    (7, 64, 1, 4000),          # whole CTAs for ragged tiles, some tiles of one unit
+    (148, 64, 30, 70),         # a CTA for every tile
+    (149, 64, 60, 130),        # one tile more than CTAs: ranges that cross tiles, entries by CTA
+    (230, 128, 1, 60),         # two tiles a query, more tiles than a block has threads
+    (1000, 16, 0, 3),          # tiles of four queries, many of them empty
+])
+def test_plans(lib, requests, hm, lo, hi):
+    rng = np.random.default_rng(requests)
+    own = [int(x) for x in rng.integers(lo, hi + 1, requests)]
+    own[-1] = hi
+    Batch(requests, own, prefix=0, page=32, hm=hm, rope=0).run_and_check(lib)
+
+
+def test_a_long_request_among_short_ones(lib):
+    for hm in (16, 64):
+        Batch(25, [3, 9000, 1, 40] + [5] * 200, prefix=0, page=64, hm=hm, rope=0).run_and_check(lib)
