@@ -219,11 +219,13 @@ constexpr int kPmScratch = kPmGrid * (int)(sizeof(int) + sizeof(TileWalk));
 static_assert(65535 * 2 <= kPmScratch / 8 * pm_threads(false), "block sums hold every row tile");
 static_assert(kPmScratch <= 3 * PmSmem<true, 512>::kSlot, "the plan's scratch");
 
-// Bounded wait of a warp that may sleep: the hint lets the hardware hold the warp
-// until the phase completes instead of answering "not yet" at once, since a dozen
-// polling warps fill the queue to shared memory that every exchange, barrier and
-// global store of the working warps goes through.
-DSA_DEVINL bool pm_try_wait(uint64_t *bar, uint32_t parity) {
+// Bounded waits. pm_wait, of the issuers and the softmax, asks again as soon as the
+// hardware answers. pm_sleep, of the loaders, gives it a hint to hold the warp until
+// the phase completes: a dozen polling warps fill the queue to shared memory that
+// every exchange, barrier and global store of the others goes through, but a warp on
+// the path from scores to products loses more by waking late (the hint everywhere
+// costs 3 to 9 %, nowhere 2 to 3 %).
+DSA_DEVINL bool pm_try_sleep(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -234,6 +236,23 @@ DSA_DEVINL bool pm_try_wait(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+
+template <bool kSleep>
+DSA_DEVINL bool pm_wait_as(PmCtl *ctl, uint64_t *bar, uint32_t parity) {
+    auto done = [&]() { return kSleep ? pm_try_sleep(bar, parity) : mbar_try_wait(bar, parity); };
+    if (done()) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (done()) return true;
+        if (ctl->abort) return false;
+        if (clock64() - t0 > kWaitLimitCycles) break;
+    }
+    raise_device_error(kErrWaitTimeout);
+    ctl->abort = 1;
+    return false;
+}
+DSA_DEVINL bool pm_wait(PmCtl *ctl, uint64_t *bar, uint32_t parity) { return pm_wait_as<false>(ctl, bar, parity); }
+DSA_DEVINL bool pm_sleep(PmCtl *ctl, uint64_t *bar, uint32_t parity) { return pm_wait_as<true>(ctl, bar, parity); }
 
 // Two probes whose answers are waited for together: bit i is set when barrier i's phase
 // of the given parity has completed, for every lane of the warp.
@@ -248,19 +267,6 @@ DSA_DEVINL uint32_t pm_test2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, u
         : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
         : "memory");
     return __reduce_and_sync(0xffffffffu, r);
-}
-
-DSA_DEVINL bool pm_wait(PmCtl *ctl, uint64_t *bar, uint32_t parity) {
-    if (pm_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-        if (pm_try_wait(bar, parity)) return true;
-        if (ctl->abort) return false;
-        if (clock64() - t0 > kWaitLimitCycles) break;
-    }
-    raise_device_error(kErrWaitTimeout);
-    ctl->abort = 1;
-    return false;
 }
 
 // One lane of a converged warp, chosen so that the compiler knows it is one:
@@ -649,16 +655,16 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             ok = pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
             const uint32_t word = __shfl_sync(0xffffffffu, ctl->unit[slot].word, 0);
             const uint32_t row0 = word & 255u;
+            const uint32_t id = tc::idesc_bf16(128, 0, true, false) | (((word >> 8) & 255u) >> 3 << 17);
+            // V^T: MN-major, 64-channel atoms kPmAtom apart, 8-token groups 1 KB apart
+            const uint64_t a0 = tc::desc_sw128(sKV + slot * S::kSlot, kPmAtom, 1024);
+            // P^T: K-major, 128-byte rows (this buffer's half), 8-row groups 1 KB apart
+            const uint64_t b0 = tc::desc_sw128(sP + row0 * 128 + pb * 64, 16, 1024);
+            if (word & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
             if (ok) ok = pm_wait(ctl, &ctl->p_full[pb], (c >> 1) & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after_sync();
-            if (word & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
             if (elect_one()) {
-                const uint32_t id = tc::idesc_bf16(128, 0, true, false) | (((word >> 8) & 255u) >> 3 << 17);
-                // V^T: MN-major, 64-channel atoms kPmAtom apart, 8-token groups 1 KB apart
-                const uint64_t a0 = tc::desc_sw128(sKV + slot * S::kSlot, kPmAtom, 1024);
-                // P^T: K-major, 128-byte rows (this buffer's half), 8-row groups 1 KB apart
-                const uint64_t b0 = tc::desc_sw128(sP + row0 * 128 + pb * 64, 16, 1024);
 #pragma unroll
                 for (int ks = 0; ks < kPmTile / 16; ++ks)
 #pragma unroll
@@ -685,7 +691,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         constexpr int kCols = kWidth / 8, kLoads = 8 * kCols / 32;         // 16 or 18 a lane
         for (int c = (warp - 4) >> 2; c < n; c += 2) {
             const int slot = c % kPmSlots, stage = c % kPmStages;
-            bool ok = pm_wait(ctl, &ctl->raw_full[stage], (c / kPmStages) & 1);
+            bool ok = pm_sleep(ctl, &ctl->raw_full[stage], (c / kPmStages) & 1);
             const UnitInfo info = ctl->raw_unit[stage];
             const uint8_t *src = gbase + S::kRaw + stage * S::kStage;
             const uint32_t dst0 = sKV + slot * S::kSlot;
@@ -700,7 +706,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 x[i] = (info.valid >> r) & 1u ? *reinterpret_cast<const uint2 *>(src + r * kWidth + 8 * col_of(i))
                                               : make_uint2(0u, 0u);
             }
-            if (ok && c >= kPmSlots) ok = pm_wait(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
+            if (ok && c >= kPmSlots) ok = pm_sleep(ctl, &ctl->kv_empty[slot], ((c / kPmSlots) - 1) & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             auto store = [&](int i, const uint32_t (&w)[4]) {
                 const int r = row_of(i), cc = col_of(i);
@@ -866,7 +872,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         if constexpr (!kFp8) {
             for (int c = grp; more; c += 2, next_slot()) {
                 const uint32_t dst0 = sKV + slot * S::kSlot;
-                const bool ok = c < kPmSlots || pm_wait(ctl, &ctl->kv_empty[slot], ph);
+                const bool ok = c < kPmSlots || pm_sleep(ctl, &ctl->kv_empty[slot], ph);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 info.valid = __ballot_sync(0xffffffffu, row >= 0);
                 bool boxes = box_rows > 0 && info.valid == 0xffffffffu;
@@ -940,7 +946,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             const auto *kv8 = reinterpret_cast<const uint8_t *>(kv);
             for (int c = grp; more; c += 2) {
                 const int stage = c % kPmStages;
-                const bool ok = c < kPmStages || pm_wait(ctl, &ctl->raw_empty[stage], ((c / kPmStages) - 1) & 1);
+                const bool ok = c < kPmStages || pm_sleep(ctl, &ctl->raw_empty[stage], ((c / kPmStages) - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 info.valid = __ballot_sync(0xffffffffu, row >= 0);
                 const int head = __shfl_sync(0xffffffffu, row, lane & 16);
