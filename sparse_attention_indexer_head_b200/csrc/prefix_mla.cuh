@@ -54,9 +54,9 @@ constexpr int kPmRows = 64;                           // (query, head) rows of a
 constexpr int kPmGrid = 148;                          // persistent CTAs, one per SM
 constexpr int kPmMinUnits = 2;                        // units a CTA takes at least
 constexpr int kPmPartUnits = 5;                       // units that a further part of a CTA costs
-// Threads: 4 softmax warps, 8 loaders, the S and PV issuers, for E4M3 2 fetchers. (Without
-// those two, registers are left for the merge kernel's blocks to wait beside a CTA.)
-constexpr int pm_threads(bool fp8) { return fp8 ? 512 : 448; }
+// Threads: 4 softmax warps, 8 loaders, the S and PV issuers, and a second S issuer for bf16,
+// two fetchers for E4M3.
+constexpr int pm_threads(bool fp8) { return fp8 ? 512 : 480; }
 constexpr int kPmIssuer = 12;
 constexpr int kPmQueries = 4;                         // queries a row tile holds at most
 
@@ -156,8 +156,10 @@ struct UnitInfo {
     DSA_DEVINL uint32_t rows() const { return (word >> 8) & 255u; }
     DSA_DEVINL bool is(uint32_t flag) const { return (word & flag) != 0; }
 };
-// First and last unit of the part; rows not yet summed; rows copied without TMA.
-enum : uint32_t { kUnitFirst = 1u << 16, kUnitLast = 2u << 16, kUnitFresh = 4u << 16, kUnitCopied = 8u << 16 };
+// First and last unit of the part; rows not yet summed; rows copied without TMA; the
+// part's number modulo 4.
+enum : uint32_t { kUnitFirst = 1u << 16, kUnitLast = 2u << 16, kUnitFresh = 4u << 16, kUnitCopied = 8u << 16,
+                  kUnitPart = 16u << 16 };
 
 struct MergeEntry { int tile, first_cta, parts, pad; };
 
@@ -179,7 +181,7 @@ constexpr uint32_t kPmSleepNs = 100000;               // hint of a wait that may
 struct PmCtl {
     uint64_t kv_full[kPmMaxSlots], kv_empty[kPmMaxSlots];
     uint64_t s_full[kPmSBufs], s_empty[kPmSBufs];
-    uint64_t p_full[2], q_full, fin;
+    uint64_t p_full[2], q_full[2], fin;
     uint64_t raw_full[kPmStages], raw_empty[kPmStages];
     UnitInfo unit[kPmMaxSlots], raw_unit[kPmStages];
     alignas(16) float alpha[kPmRows], linv[kPmRows];
@@ -559,8 +561,9 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             mbar_init(&ctl->raw_full[i], 1);
             mbar_init(&ctl->raw_empty[i], 4);
         }
-        mbar_init(&ctl->q_full, 128);
-        mbar_init(&ctl->fin, 2);
+        mbar_init(&ctl->q_full[0], 128);
+        mbar_init(&ctl->q_full[1], 128);
+        mbar_init(&ctl->fin, kFp8 ? 2 : 3);       // a commit of every issuer
         ctl->abort = 0;
         ctl->last_tile = -1;
         fence_mbarrier_init();
@@ -600,28 +603,34 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         merge[blockIdx.x] = e;
     }
 
-    if (warp == kPmIssuer) {
-        // ------------------------------------------------------------------ S issuer
-        // S(c)[64 rows x 32 tokens] = Q K^T, kWidth / 16 K-steps. Two S buffers let it
-        // run up to two units ahead of PV. The waits are blocking and in a fixed order,
-        // in a warp of its own: with the pipe reading operands, one access to shared
-        // memory takes over 100 cycles, and a loop that polls for either product
-        // spent 600 cycles a turn.
+    if (warp == kPmIssuer || (!kFp8 && warp == kPmIssuer + 2)) {
+        // ------------------------------------------------------------------ S issuers
+        // S(c)[64 rows x 32 tokens] = Q K^T, kWidth / 16 K-steps, up to two units
+        // ahead of PV. While the tensor cores read their operands an access to shared memory
+        // takes over 100 cycles: two waits and the unit's word take an issuer 650 of 1290
+        // cycles a unit. bf16 therefore has two of them, for even and for odd units (64
+        // requests behind 16384 tokens 387 -> 372 us, 64 of two queries behind 16389 112 ->
+        // 108 us; one row of 512 11.8 -> 12.3 us); E4M3 does better with the warp as a second
+        // fetcher (64 ragged requests 262 us, with one fetcher and two issuers 292 us).
         constexpr uint32_t idS = tc::idesc_bf16(64, kPmTile, false, false);
         const uint64_t a0 = tc::desc_sw128(sQ, 16, 1024);
+        constexpr int kStep = kFp8 ? 1 : 2;
         bool ok = true;
-        int parts = 0, slot = 0;
-        for (int c = 0; c < n; ++c) {
-            const int sb = c % kPmSBufs;
+        uint32_t seen = 4u;                               // part of this warp's last unit
+        for (int c = (warp - kPmIssuer) >> 1; c < n; c += kStep) {
+            const int slot = c % kPmSlots, sb = c & 1;
+            const uint32_t d = tmem + kPmSCol + (uint32_t)(sb * kPmTile);
             ok = pm_wait(ctl, &ctl->kv_full[slot], (c / kPmSlots) & 1);
-            const uint32_t word = ctl->unit[slot].word;
-            if (ok && c >= kPmSBufs) ok = pm_wait(ctl, &ctl->s_empty[sb], ((c / kPmSBufs) - 1) & 1);
-            if (ok && (word & kUnitFirst)) ok = pm_wait(ctl, &ctl->q_full, parts++ & 1);
+            const uint32_t word = ctl->unit[slot].word, part = word / kUnitPart & 3u;
+            if (ok && c >= 2) ok = pm_wait(ctl, &ctl->s_empty[sb], ((c >> 1) - 1) & 1);
+            // Parts alternate two barriers: a part whose only unit went to the other warp
+            // passes unseen here, and its barrier then does not stand for the next one's.
+            if (ok && part != seen) ok = pm_wait(ctl, &ctl->q_full[part & 1], part >> 1);
+            seen = part;
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after_sync();
             if (word & kUnitCopied) tc::fence_proxy_async_smem();   // cp.async writes, tensor-core reads
             if (elect_one()) {
-                const uint32_t d = tmem + kPmSCol + (uint32_t)(sb * kPmTile);
                 const uint64_t b0 = tc::desc_sw128(sKV + slot * S::kSlot, 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kPmQSteps; ++kk)
@@ -637,7 +646,6 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 tc::mma_commit(&ctl->s_full[sb]);
             }
             __syncwarp();
-            if (++slot == kPmSlots) slot = 0;
         }
         __syncwarp();
         if (elect_one()) tc::mma_commit(&ctl->fin);
@@ -759,6 +767,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         TileWalk w;
         int tile = n > 0 ? ctl->first_tile : 0, u = n > 0 ? ctl->first_unit : 0;
         int part_begin = u;                               // the part's first unit in its tile
+        const int tile0 = tile;
         if (n > 0) w = ctl->first;
         long long global_unit = ctl->begin;
         int left = n;                                     // units from the current one on
@@ -821,7 +830,8 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             const bool first = u == part_begin, last = left == 1 || u + 1 == w.units;
             const bool summed = (w.shared && part_begin < w.npre) || ((seg & 1) && ((met >> (seg >> 1)) & 1));
             const bool fresh = first || (seg >= 0 && seg_first && !summed);
-            info.word = rows_word | (first ? kUnitFirst : 0u) | (last ? kUnitLast : 0u) | (fresh ? kUnitFresh : 0u);
+            info.word = rows_word | (first ? kUnitFirst : 0u) | (last ? kUnitLast : 0u) | (fresh ? kUnitFresh : 0u) |
+                        (uint32_t)((tile - tile0) & 3) * kUnitPart;
             // read on the last unit alone: a part that is the whole tile has no slot
             info.part = part_begin == 0 && u + 1 == w.units ? -1 : 2 * (int)blockIdx.x + (part_begin == 0 ? 1 : 0);
             const int t = tok0 + lane;
@@ -1040,16 +1050,16 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             }
             tc::tmem_wait_st();
         };
-        auto release_q = [&]() {
+        auto release_q = [&](int tile) {
             tc::cp_async_wait_all();
             tc::fence_proxy_async_smem();
             tc::fence_before_sync();
-            mbar_arrive(&ctl->q_full);
+            mbar_arrive(&ctl->q_full[(tile - ctl->first_tile) & 1]);
         };
         int tile = n > 0 ? ctl->first_tile : 0;       // a CTA's parts are consecutive row tiles
         if (n > 0) {
             load_q(tile);
-            release_q();
+            release_q(tile);
         }
         // Ring positions and parities of units c, c - 1 and c - 2 (a PV frees its slot,
         // and has then read its P buffer).
@@ -1198,7 +1208,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 }
                 break;
             }
-            release_q();
+            release_q(tile + 1);
             tc::fence_after_sync();
 #pragma unroll 1
             for (int blk = 0; blk < 8; ++blk)
