@@ -386,6 +386,8 @@ class PrefixDecode:
         self.cache = torch.zeros(self.kv_rows, self.width, dtype=torch.uint8 if fp8 else torch.bfloat16, **dev)
         i32 = dict(dtype=torch.int32, device=self.device)
         self.prefix_tokens = torch.tensor([prefix_len], **i32)
+        self.prefix_req = torch.zeros(prefix_len, **i32)
+        self.prefix_pos = torch.arange(prefix_len, **i32)
         self.seq_len = torch.full((requests,), prefix_len, **i32)
         self.q_req = torch.arange(requests, **i32)
         self.q_pos = self.seq_len - 1
@@ -410,12 +412,18 @@ class PrefixDecode:
         else:
             B.dsa_latent_append_paged(kv_new, *shape, self.cache, self.kv_rows, *queries, stream=stream)
 
+    @staticmethod
+    def _check(name: str, x: torch.Tensor, shape) -> None:
+        if tuple(x.shape) != shape or x.dtype != torch.bfloat16:
+            raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)}, not bfloat16 {shape}")
+
     def fill_prefix(self, kv_new: torch.Tensor, stream=None) -> None:
         """Append the prefix's rows: kv_new bf16 [prefix_len, 512 + rope], as projected."""
-        if tuple(kv_new.shape) != (self.prefix_len, self.width):
-            raise ValueError(f"kv_new is {tuple(kv_new.shape)}, not {(self.prefix_len, self.width)}")
-        pos = torch.arange(self.prefix_len, dtype=torch.int32, device=self.device)
-        self._append(kv_new, torch.zeros_like(pos), pos, self.prefix_table, 1, stream=stream)
+        self._check("kv_new", kv_new, (self.prefix_len, self.width))
+        if kv_new.device != self.cache.device or kv_new.stride(1) != 1:
+            raise ValueError("kv_new must lie on the cache's device, the channels of a row together")
+        with torch.cuda.device(self.device):
+            self._append(kv_new, self.prefix_req, self.prefix_pos, self.prefix_table, 1, stream=stream)
 
     def _calls(self, stream=None):
         self._append(self.kv_new, self.q_req, self.q_pos, self.block_table, self.requests, self.q, stream)
@@ -434,6 +442,12 @@ class PrefixDecode:
         [requests, heads, 512] (its buffer, overwritten by the next step)."""
         if self.prefix_len + self.tokens >= self.max_len:
             raise ValueError("the requests' pages are full")
+        self._check("kv_new", kv_new, tuple(self.kv_new.shape))
+        self._check("q", q, tuple(self.q.shape))
+        with torch.cuda.device(self.device):
+            return self._step(kv_new, q)
+
+    def _step(self, kv_new: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
         self.kv_new.copy_(kv_new, non_blocking=True)
         self.q.copy_(q, non_blocking=True)
         self.seq_len += 1

@@ -375,3 +375,24 @@ def test_pipeline_prefix_decode_refuses(lib):
     dec.step(*row)
     with pytest.raises(ValueError):
         dec.step(*row)
+
+
+def test_pipeline_prefix_decode_refuses_other_shapes(lib):
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    dec = PrefixDecode(2, 16, 4, 4, norm_w=None)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):                     # the channels of a row apart
+        dec.fill_prefix(torch.zeros(512, 4, **bf).t())
+    with pytest.raises(ValueError):
+        dec.fill_prefix(torch.zeros(4, 512, device="cuda"))
+    with pytest.raises(ValueError):
+        dec.fill_prefix(torch.zeros(4, 512, dtype=torch.bfloat16))
+    kv_new, q = torch.zeros(2, 512, **bf), torch.zeros(2, 16, 512, **bf)
+    for bad in [(kv_new[:1], q), (kv_new, q[:, :1]), (kv_new, q[0]), (kv_new.float(), q), (kv_new, q.half())]:
+        with pytest.raises(ValueError):
+            dec.step(*bad)
+    assert dec.tokens == 0
+    # rows of a wider projection
+    dec.fill_prefix(torch.ones(4, 1024, **bf)[:, 512:])
+    torch.cuda.synchronize()
+    assert (dec.cache[:4] == 1).all()

@@ -113,6 +113,23 @@ def test_large_and_negative_logits(lib):
     b.run_and_check(lib)
 
 
+@pytest.mark.parametrize("own", [40, 5000])              # one part, and parts that are merged
+def test_infinite_logits(lib, own):
+    # channel 9 of every row is 1: head 1's logits are all -infinity, head 2's all +infinity
+    b = Batch(26, [own], page=32, hm=16, rope=0)
+    b.values[:, 9] = 1.0
+    clean = b.oracle()
+    b.q[0, 1, 9], b.q[0, 2, 9] = -np.inf, np.inf
+    d, o = b.device(), b.buffers(lib)
+    b.call(lib, d, o)
+    torch.cuda.synchronize()
+    out, lse = o["out"].float().cpu().numpy(), o["lse"].cpu().numpy()
+    rest = [h for h in range(16) if h not in (1, 2)]
+    assert_attention_close(out[:, rest], lse[:, rest], [x if i == 4 else x[:, rest] for i, x in enumerate(clean)], b.width)
+    assert (out[0, 1] == 0).all() and np.isneginf(lse[0, 1])
+    assert np.isnan(out[0, 2]).all() and np.isnan(lse[0, 2])
+
+
 def test_rows_that_grow_along_the_sequence(lib):
     # every later token has a larger logit: each tile raises the maximum of every row
     b = Batch(10, [700], prefix=0, page=64, hm=64, rope=0)
