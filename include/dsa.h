@@ -459,8 +459,10 @@ int dsa_sparse_mla_decode_noalloc(const dsa_bf16 *q, const dsa_bf16 *kv, int64_t
  *              channels of head h of token i at q_rot + i * q_tok_stride +
  *              h * q_head_stride (multiples of 8), rotated like the row's and
  *              written to columns kv_lora .. of q, bf16 [n, Hm, kv_lora +
- *              rope_dim]; its first kv_lora columns are not touched. q_rot may
- *              be q + kv_lora itself (rotated in place); no other overlap.
+ *              rope_dim]; its first kv_lora columns are not touched. A token's
+ *              heads lie together (q_tok_stride >= (Hm - 1) * q_head_stride +
+ *              rope_dim). q_rot may be q + kv_lora itself (rotated in place); no
+ *              other overlap, of kv_new and kv included.
  * Arithmetic is fp32, rounded once to the cache's type.
  * A token is skipped, row and heads, when its request is outside [0, B), its
  * position negative or, with rope_dim > 0, not below max_pos; its row alone is
@@ -485,7 +487,8 @@ int dsa_latent_append_paged(const dsa_bf16 *kv_new, int64_t kv_new_stride, const
  * g1 into an fp8 latent cache, the layout of dsa_sparse_mla_decode_paged_fp8:
  *   kv8        uint8 [kv_rows, kv_lora + rope_dim]: code = E4M3(value * (1 /
  *              kv_scale)), rounded to nearest even, saturated at +-448, NaN
- *              kept; kv_scale finite and > 0.
+ *              kept; kv_scale and its reciprocal finite and > 0
+ *              (DSA_ERR_INVALID_ARG otherwise).
  * Everything else as dsa_latent_append_paged (the query heads stay bf16).
  */
 int dsa_latent_append_paged_fp8(const dsa_bf16 *kv_new, int64_t kv_new_stride,
@@ -522,9 +525,12 @@ int dsa_latent_append_paged_fp8(const dsa_bf16 *kv_new, int64_t kv_new_stride,
  *   kv_lora + rope_dim channels, out[i,h,:] = bf16(sum_t softmax(z)_t *
  *   kv[row(t), :kv_lora]), lse[i,h] = log(sum_t exp(z_t)) (natural; out = 0 and
  *   -inf when the query sees no token). lse may be NULL. Precision: the P.V
- *   product takes the softmax weights as bf16 (an output moves by at most 2^-9
- *   of the largest value in its channel); sums, maxima and the parts of a
- *   sequence that are merged stay fp32.
+ *   product takes the softmax weights as bf16 (each off by at most 2^-8 of
+ *   itself, so an output moves by at most 2^-8 of the largest value in its
+ *   channel); sums, maxima and the parts of a sequence that are merged stay
+ *   fp32. A head whose logits are all -infinity counts as one that sees no
+ *   token; a NaN or +infinity among them gives NaN.
+ *   out, lse and workspace overlap neither one another nor an input.
  *   workspace: device scratch of dsa_prefix_mla_workspace_size(Q, Hm) bytes
  *   (16-byte aligned, no initialisation; not shared between calls that may
  *   overlap, two captured graphs among them).
@@ -532,7 +538,8 @@ int dsa_latent_append_paged_fp8(const dsa_bf16 *kv_new, int64_t kv_new_stride,
  * tables and a prefix of another length. Results do not depend on scheduling.
  * Requires kv_lora == 512, rope_dim 0 or 64, Hm a multiple of 16 with 16 <= Hm
  * <= 128, Q <= 65535, kv_rows <= INT32_MAX (DSA_ERR_UNSUPPORTED otherwise),
- * page_size >= 1, prefix_blocks and max_blocks >= 0 (DSA_ERR_INVALID_ARG).
+ * page_size >= 1, prefix_blocks and max_blocks >= 0, sm_scale * log2(e) finite
+ * in fp32 (DSA_ERR_INVALID_ARG).
  * Q == 0 launches nothing. Nothing is read before the wait on the preceding
  * kernel.
  */
@@ -551,7 +558,8 @@ int dsa_prefix_mla_decode_paged(const dsa_bf16 *q, const dsa_bf16 *kv, int64_t k
  * codes and one fp32 scale, latent value = kv_scale * E4M3(code), as for
  * dsa_sparse_mla_decode_paged_fp8 (codes widened to bf16, which is exact; the
  * scale applied to the logits and the output). DSA_ERR_INVALID_ARG for a
- * kv_scale that is not finite and positive.
+ * kv_scale that is not finite and positive, or whose product with sm_scale *
+ * log2(e) is not finite.
  */
 int dsa_prefix_mla_decode_paged_fp8(const dsa_bf16 *q, const uint8_t *kv8, float kv_scale,
                                     int64_t kv_rows, const int32_t *prefix_table,

@@ -1,7 +1,33 @@
 // Dense MLA over a block-table paged latent cache for a batch whose requests
 // share a prefix ("spark_model/layers/glm5next_dsa/mod.rs": the serve path's
 // block-table paged MLA decode, walking 0..seq_len instead of a selected-index
-// row). Plain form: one warp per (query, head), online softmax over the tokens.
+// row).
+//
+//   z_t = sm_scale <q, kv_t>,   out = sum_t e^z_t v_t / sum_t e^z_t,   lse = log sum_t e^z_t
+// over the tokens t that a (query, head) row sees; v_t are the first 512 channels of the
+// row kv_t. With m the running maximum (lazily kept: within 2^8 of the true one), l the
+// running sum and O the running sum of e^(z_t - m) v_t, a further token multiplies l and O
+// by e^(m - m') where m grows to m'; two parts (m, l, O) merge the same way, so a sequence
+// may be cut anywhere.
+//
+// Row tile: 64 (query, head) rows, of one query's heads or of up to four queries of fewer
+// heads. Rows that share tokens thus share the copies of them: the prefix is read once for
+// a tile's queries (and by the 148 CTAs together from L2), and draft tokens of one request
+// share their history. Unit: 32 tokens, on the fifth-generation tensor cores
+//   S[64 x 32]     = Q K^T       M = 64, N = 32;  Q's first 384 channels in tensor memory
+//   O^T[512 x 64] += V^T P^T     4 blocks of M = 128, N = 64, from the same copy of the rows:
+// a row is K (K-major) and V (MN-major) of one swizzled tile. Persistent: one CTA an SM,
+// which works out on the device which units of which row tiles are its own (pm_plan).
+//
+// What bounds it: the tensor cores read their operands from shared memory at 128 bytes a
+// cycle, which for tiles of 64 rows takes 1103 cycles a unit with rope (S 24 x 16.4 + 12 x
+// 24.5, PV 8 x 48.5), and the copies write it too. A unit takes about 1240 cycles (S in two
+// issuers), 1290 with E4M3's single issuer; long batches run at 0.78 PFLOP/s (64 requests of
+// 128 heads behind 16384 tokens: 372 us). A request of one row tile over 131072 tokens is
+// bound by HBM instead (4 of them 115 us, 4.7 TB/s). A call's start takes about 4 us (the
+// chain lengths -> plan -> page table -> rows -> first product), the output of a part 2.5
+// us and the merge 2.5 to 8 us: 11.8 us for a row of 512 tokens, 37 us for 16 requests
+// behind 6144.
 #pragma once
 
 #include "common.cuh"
@@ -879,8 +905,9 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         UnitInfo info;
         int row = -1;
         if (more) row = describe(info);
+        int c = grp;                                      // behind the loop: the first unit not copied
         if constexpr (!kFp8) {
-            for (int c = grp; more; c += 2, next_slot()) {
+            for (; more; c += 2, next_slot()) {
                 const uint32_t dst0 = sKV + slot * S::kSlot;
                 const bool ok = c < kPmSlots || pm_sleep(ctl, &ctl->kv_empty[slot], ph);
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -954,7 +981,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             // A unit's rows lie one after the other within a page: one bulk copy for 32
             // rows of one page, two for halves, else one a row.
             const auto *kv8 = reinterpret_cast<const uint8_t *>(kv);
-            for (int c = grp; more; c += 2) {
+            for (; more; c += 2) {
                 const int stage = c % kPmStages;
                 const bool ok = c < kPmStages || pm_sleep(ctl, &ctl->raw_empty[stage], ((c / kPmStages) - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -982,6 +1009,13 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 more = advance() && advance();
                 if (more) row = describe(info);
             }
+        }
+        if (ctl->abort && sub == 0) {
+            // A wait ran out: the bulk copies under way land before the block leaves its shared
+            // memory. (A slot's earlier unit was released before its next one was copied.)
+            constexpr int kRing = kFp8 ? kPmStages : kPmSlots;
+            for (int k = c - 2; k >= 0 && k > c - 2 - kRing; k -= 2)
+                (void)mbar_wait(kFp8 ? &ctl->raw_full[k % kRing] : &ctl->kv_full[k % kRing], (k / kRing) & 1);
         }
         if (begins) enter_tile(ctl->first_tile, ctl->begin, ctl->first_units);
         tc::cp_async_wait_all();          // nothing of this warp in flight past here
@@ -1435,6 +1469,8 @@ inline int prefix_mla_launch(const void *q, const void *kv, float kv_scale, int6
     if (!(sm_scale == sm_scale) || sm_scale == INFINITY || sm_scale == -INFINITY)
         return DSA_ERR_INVALID_ARG;
     if (kFp8 && !(kv_scale > 0.f && kv_scale < INFINITY)) return DSA_ERR_INVALID_ARG;
+    const float scale_log2 = (kFp8 ? sm_scale * kv_scale : sm_scale) * 1.4426950408889634f;
+    if (!(fabsf(scale_log2) < INFINITY)) return DSA_ERR_INVALID_ARG;
     if (kv_lora != DSA_KV_LORA || (rope != 0 && rope != kRopeDim) || Hm % 16 != 0 ||
         Hm > DSA_MAX_MLA_HEADS)
         return DSA_ERR_UNSUPPORTED;
@@ -1454,7 +1490,6 @@ inline int prefix_mla_launch(const void *q, const void *kv, float kv_scale, int6
     g.page_shift = -1;
     if ((g.page & (g.page - 1)) == 0)
         for (g.page_shift = 0; (1 << g.page_shift) < g.page;) ++g.page_shift;
-    const float scale_log2 = (kFp8 ? sm_scale * kv_scale : sm_scale) * 1.4426950408889634f;
     const float out_scale = kFp8 ? kv_scale : 1.0f;
     return rope ? prefix_mla_run<kFp8, DSA_KV_LORA + kRopeDim>(q, kv, g, Hm, scale_log2, out_scale,
                                                                out, lse, ws, stream)

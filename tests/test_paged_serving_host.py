@@ -49,7 +49,7 @@ def test_append_refusals(B, bad, status, fp8):
 
 
 def test_append_scale_and_empty_calls(B):
-    for scale in (0.0, -1.0, float("inf"), float("nan")):
+    for scale in (0.0, -1.0, float("inf"), float("nan"), 1e-39):     # 1 / 1e-39 is no fp32 number
         assert _append(B, True, scale=scale) == B.DSA_ERR_INVALID_ARG
     none = dict(kv_new=None, tok_req=None, tok_pos=None, table=None, kv=None, cos_sin=None)
     assert _append(B, n=0, **none) == B.DSA_OK
@@ -90,6 +90,8 @@ def test_prefix_mla_refusals(B, bad, status, fp8):
 def test_prefix_mla_scale_empty_call_and_workspace(B):
     for scale in (0.0, -1.0, float("inf"), float("nan")):
         assert _mla(B, True, scale=scale) == B.DSA_ERR_INVALID_ARG
+    assert _mla(B, True, scale=1e30, sm=-1e30) == B.DSA_ERR_INVALID_ARG     # the logits' scale overflows
+    assert _mla(B, sm=3e38) == B.DSA_ERR_INVALID_ARG                        # with its log2(e) too
     assert _mla(B, Q=0, q=None, q_req=None, out=None, ws=None) == B.DSA_OK
     assert B.dsa_prefix_mla_workspace_size(0, 64) == 0
     for Q, hm in [(1, 16), (64, 128), (65535, 128)]:
