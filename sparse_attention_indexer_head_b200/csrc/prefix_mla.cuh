@@ -30,6 +30,8 @@
 // behind 6144.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "latent_append.cuh"
 #include "sparse_mla.cuh"
@@ -204,6 +206,8 @@ constexpr int kPmMaxSlots = 6;
 constexpr int kPmStages = 4;                          // E4M3 units in flight
 constexpr uint32_t kPmSleepNs = 100000;               // hint of a wait that may sleep
 
+constexpr int kPlanWarps = (kPmGrid + 31) / 32;       // whose threads have row tiles that CTAs are given to
+
 struct PmCtl {
     uint64_t kv_full[kPmMaxSlots], kv_empty[kPmMaxSlots];
     uint64_t s_full[kPmSBufs], s_empty[kPmSBufs];
@@ -214,9 +218,9 @@ struct PmCtl {
     // The plan: this CTA's first row tile and unit, its units, and for a row tile that
     // it begins, the CTAs that hold it (0: worked out from per and begin).
     long long warp_sum[16];
+    uint2 warp_need[kPlanWarps];                      // CTAs, longest range of 32 row tiles
     long long total, per, begin;
     int first_tile, first_unit, first_units, count, parts;
-    int whole_ctas;
     TileWalk first;                                   // of first_tile
     // The last part, written out by all warps.
     int last_tile, last_part;
@@ -243,9 +247,9 @@ static_assert(PmSmem<false, 576>::kBytes <= 232448 && PmSmem<false, 512>::kBytes
                   PmSmem<true, 576>::kBytes <= 232448 && PmSmem<true, 512>::kBytes <= 232448,
               "shared memory per block");
 static_assert(PmSmem<false, 512>::kSlots <= kPmMaxSlots, "ring");
-constexpr int kPmScratch = kPmGrid * (int)(sizeof(int) + sizeof(TileWalk));
-static_assert(65535 * 2 <= kPmScratch / 8 * pm_threads(false), "block sums hold every row tile");
-static_assert(kPmScratch <= 3 * PmSmem<true, 512>::kSlot, "the plan's scratch");
+constexpr int kPmScratch = (65535 * 2 + pm_threads(false) - 1) / pm_threads(false) * 8;   // a sum a block of row tiles
+static_assert(kPmScratch <= PmSmem<true, 512>::kSlot, "the plan's scratch");
+static_assert(kPlanWarps * 32 <= pm_threads(false), "a thread a row tile");
 
 // Bounded waits. pm_wait, of the issuers and the softmax, asks again as soon as the
 // hardware answers. pm_sleep, of the loaders, gives it a hint to hold the warp until
@@ -355,13 +359,9 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
             w.load(g, rt, tid, P);
             units = w.units;
         }
-        if (tid < kPmGrid) {
-            reinterpret_cast<int *>(scratch)[tid] = units;
-            if (tid < rt.count) reinterpret_cast<TileWalk *>(reinterpret_cast<int *>(scratch) + kPmGrid)[tid] = w;
-        }
         inc = warp_inclusive_sum((unsigned)units, lane);   // of 32 tiles of at most 2^26 units
         if (lane == 31) ctl->warp_sum[warp] = inc;
-        if (tid == 0) ctl->count = ctl->parts = ctl->whole_ctas = 0;
+        if (tid == 0) ctl->count = ctl->parts = 0;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
@@ -371,7 +371,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
     } else {
         auto *block_sum = reinterpret_cast<long long *>(scratch);
         for (int k = tid; k < nb; k += kThreads) block_sum[k] = 0;
-        if (tid == 0) ctl->count = ctl->parts = ctl->whole_ctas = 0;
+        if (tid == 0) ctl->count = ctl->parts = 0;
         __syncthreads();
         for (int k = 0; k < nb; ++k) {
             const int t = k * kThreads + tid;
@@ -399,57 +399,42 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
         ctl->begin = begin;
     }
     if (rt.count > 1 && rt.count <= G && total < (1 << 24)) {
-        // 1 + floor(units (G - count) / total) CTAs for a row tile: no more than G in all.
-        // By reciprocals, short of the quotient here and above it for the range a CTA takes.
-        if (warp == 0) {
-            const auto *tile_units = reinterpret_cast<const unsigned *>(scratch);
+        // Thread t: 1 + floor(units (G - count) / total) CTAs for row tile t, no more than G
+        // in all, and the longest range that they get. By reciprocals, short of the quotient
+        // here and above it for the range. (By a thread a row tile: code that a CTA runs once
+        // comes from memory, and one warp's unrolled loops over the row tiles took 1.3 us.)
+        unsigned need = 0, each = 0;
+        if (tid < rt.count) {
             const float share = (float)(G - rt.count) * rcp_approx((float)total) * (1.f - 0x1p-20f);
-            // lane l: consecutive row tiles, up to five; their CTAs and longest range
-            constexpr int kEach = (kPmGrid + 31) / 32;
-            const int lane_tiles = (rt.count + 31) / 32;
-            unsigned need[kEach], each[kEach], sum = 0, longest = 0;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                need[i] = each[i] = 0;
-                const int t = lane * lane_tiles + i;
-                if (i < lane_tiles && t < rt.count) {
-                    const unsigned u = tile_units[t];
-                    need[i] = 1u + (unsigned)((float)u * share);
-                    each[i] = (unsigned)((float)u * rcp_approx((float)need[i]) * (1.f + 0x1p-20f)) + 1u;
-                    each[i] = max(each[i], (unsigned)kPmMinUnits);
-                    if (need[i] == 1u) each[i] = u;
-                }
-                sum += need[i];
-                longest = max(longest, each[i]);
-            }
-            longest = __reduce_max_sync(0xffffffffu, longest);
-            if (longest < (unsigned)per + kPmPartUnits) {
-                unsigned before = warp_inclusive_sum(sum, lane) - sum;
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const unsigned k = blockIdx.x - before;
-                    if (k < need[i]) {
-                        const int t = lane * lane_tiles + i;
-                        const unsigned u = tile_units[t];
-                        unsigned parts = (unsigned)((float)u * rcp_approx((float)each[i]));
-                        while (parts * each[i] < u) ++parts;
-                        while (parts > 1 && (parts - 1) * each[i] >= u) --parts;
-                        ctl->first_tile = t;
-                        ctl->first = reinterpret_cast<const TileWalk *>(tile_units + kPmGrid)[t];
-                        ctl->first_unit = (int)min(u, k * each[i]);
-                        ctl->first_units = (int)u;
-                        ctl->count = (int)(u - min(u, k * each[i]));
-                        ctl->count = min(ctl->count, (int)each[i]);
-                        ctl->parts = (int)parts;
-                    }
-                    before += need[i];
-                }
-                if (lane == 0) ctl->whole_ctas = 1;
-            }
+            need = 1u + (unsigned)((float)units * share);
+            each = need == 1u ? (unsigned)units
+                              : max((unsigned)((float)units * rcp_approx((float)need) * (1.f + 0x1p-20f)) + 1u,
+                                    (unsigned)kPmMinUnits);
         }
+        const unsigned inc_need = warp_inclusive_sum(need, lane);
+        const unsigned longest_w = __reduce_max_sync(0xffffffffu, each);
+        if (lane == 31 && warp < kPlanWarps) ctl->warp_need[warp] = make_uint2(inc_need, longest_w);
         __syncthreads();
-        if (ctl->whole_ctas) {
-            tc::fence_proxy_async_smem();             // the scratch becomes the ring
+        unsigned k = blockIdx.x - (inc_need - need), longest = 0;
+#pragma unroll
+        for (int i = 0; i < kPlanWarps; ++i) {
+            const uint2 x = ctl->warp_need[i];
+            k -= i < warp ? x.x : 0u;
+            longest = max(longest, x.y);
+        }
+        if (longest < (unsigned)per + kPmPartUnits) {
+            if (k < need) {
+                const unsigned u = (unsigned)units, at = min(u, k * each);
+                unsigned parts = (unsigned)((float)u * rcp_approx((float)each));
+                while (parts * each < u) ++parts;
+                while (parts > 1 && (parts - 1) * each >= u) --parts;
+                ctl->first_tile = tid;
+                ctl->first = w;
+                ctl->first_unit = (int)at;
+                ctl->first_units = units;
+                ctl->count = (int)min(u - at, each);
+                ctl->parts = (int)parts;
+            }
             __syncthreads();
             return;
         }
@@ -1037,7 +1022,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         // K-major), the others into tensor memory, where this thread's row hh has its
         // pairs of channels as columns: thread and partner load alternate 16-byte
         // vectors (four columns) and swap the columns of the other's parity.
-        auto load_q = [&](int tile) {
+        auto load_q = [&](int tile, auto batch) {
             const int row0 = rt.first_row(tile), nr = rt.rows(tile);
             constexpr int kPieces = S::kQAtoms * 8;
 #pragma unroll 2
@@ -1050,9 +1035,11 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                     tc::st_shared_zero16(dst);
             }
             const uint4 *src = reinterpret_cast<const uint4 *>(q + (size_t)(row0 + min(hh, nr - 1)) * kWidth) + par;
-            // Batches of two 32-column blocks. (Two batches in flight spill, and the loop over
-            // the units then pays for it.)
-            constexpr int kBlocks = kPmQSteps * 8 / 32, kBatch = 2;
+            // Batches of 32-column blocks, a batch's loads in flight at once: the first row
+            // tile's are what a CTA waits for, a later one's hide behind its last PV and have
+            // fewer registers (two batches in flight spill there).
+            constexpr int kBlocks = kPmQSteps * 8 / 32, kBatch = decltype(batch)::value;
+            static_assert(kBlocks % kBatch == 0, "whole batches");
 #pragma unroll
             for (int b0 = 0; b0 < kBlocks; b0 += kBatch) {
                 uint4 x[kBatch][4];
@@ -1092,7 +1079,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
         };
         int tile = n > 0 ? ctl->first_tile : 0;       // a CTA's parts are consecutive row tiles
         if (n > 0) {
-            load_q(tile);
+            load_q(tile, std::integral_constant<int, 3>{});
             release_q(tile);
         }
         // Ring positions and parities of units c, c - 1 and c - 2 (a PV frees its slot,
@@ -1223,7 +1210,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
             // the part is done: the next row tile's queries are loaded while the last PV
             // runs, and its products start behind this part's output.
             const bool more = c + 1 < n;
-            if (more) load_q(tile + 1);
+            if (more) load_q(tile + 1, std::integral_constant<int, 2>{});
             bad = !pm_wait(ctl, &ctl->kv_empty[cslot], cpar);   // the part's last PV
             if (owner) ctl->linv[hh] = l != 0.f ? out_scale / l : 0.f;
             if (tc::named_bar_or(2, 128, bad)) { failed = true; break; }
