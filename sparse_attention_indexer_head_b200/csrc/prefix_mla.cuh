@@ -965,34 +965,28 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                 if (more) row = describe(info);           // its page lookups run behind this unit's copies
             }
         } else {
-            // A unit's rows lie one after the other within a page: one bulk copy for 32
-            // rows of one page, two for halves, else one a row.
+            // A bulk copy for every run of rows that lie one after the other: one for a unit
+            // within a page, up to three with pages of 16 or more rows of any number.
             const auto *kv8 = reinterpret_cast<const uint8_t *>(kv);
             for (; more; c += 2) {
                 const int stage = c % kPmStages;
                 const bool ok = c < kPmStages || pm_sleep(ctl, &ctl->raw_empty[stage], ((c / kPmStages) - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 info.valid = __ballot_sync(0xffffffffu, row >= 0);
-                const int head = __shfl_sync(0xffffffffu, row, lane & 16);
-                const int row_a = __shfl_sync(0xffffffffu, row, 0);
-                const bool halves = __all_sync(0xffffffffu, row >= 0 && row == head + (lane & 15));
-                const bool whole = halves && __all_sync(0xffffffffu, row == row_a + lane);
+                const int prev = __shfl_up_sync(0xffffffffu, row, 1);
+                const bool begins_run = row >= 0 && (lane == 0 || prev < 0 || row != prev + 1);
+                // the lanes that end a run before them
+                const uint32_t ends = __ballot_sync(0xffffffffu, begins_run || row < 0) & (0xfffffffeu << lane);
                 uint8_t *dst = gbase + S::kRaw + stage * S::kStage;
                 if (elect_one()) {
                     ctl->raw_unit[stage] = info;
                     mbar_arrive_expect_tx(&ctl->raw_full[stage], __popc(info.valid) * kWidth);
-                    if (whole) bulk_g2s(dst, kv8 + (size_t)row_a * kWidth, kPmTile * kWidth, &ctl->raw_full[stage]);
                 }
                 __syncwarp();
-                if (!whole) {
-                    if (halves) {
-                        if ((lane & 15) == 0)
-                            bulk_g2s(dst + lane * kWidth, kv8 + (size_t)row * kWidth, 16 * kWidth, &ctl->raw_full[stage]);
-                    } else if (row >= 0) {
-                        bulk_g2s(dst + lane * kWidth, kv8 + (size_t)row * kWidth, kWidth, &ctl->raw_full[stage]);
-                    }
-                    __syncwarp();
-                }
+                if (begins_run)
+                    bulk_g2s(dst + lane * kWidth, kv8 + (size_t)row * kWidth, ((ends ? __ffs(ends) - 1 : 32) - lane) * kWidth,
+                             &ctl->raw_full[stage]);
+                __syncwarp();
                 more = advance() && advance();
                 if (more) row = describe(info);
             }
