@@ -205,7 +205,7 @@ constexpr uint32_t kPmAtom = kPmTile * 128;           // 64 channels of a slot's
 constexpr uint32_t kPmPBytes = kPmRows * 128;         // two P buffers, the halves of 128-byte rows
 static_assert(kPmQCol + kPmQSteps * 8 <= 512, "tensor memory columns");
 constexpr int kPmMaxSlots = 6;
-constexpr int kPmStages = 4;                          // E4M3 units in flight
+constexpr int kPmMaxStages = 4;
 constexpr uint32_t kPmSleepNs = 100000;               // hint of a wait that may sleep
 
 constexpr int kPlanWarps = (kPmGrid + 31) / 32;       // whose threads have row tiles that CTAs are given to
@@ -214,8 +214,8 @@ struct PmCtl {
     uint64_t kv_full[kPmMaxSlots], kv_empty[kPmMaxSlots];
     uint64_t s_full[kPmSBufs], s_empty[kPmSBufs];
     uint64_t p_full[2], q_full[2], fin;
-    uint64_t raw_full[kPmStages], raw_empty[kPmStages];
-    UnitInfo unit[kPmMaxSlots], raw_unit[kPmStages];
+    uint64_t raw_full[kPmMaxStages], raw_empty[kPmMaxStages];
+    UnitInfo unit[kPmMaxSlots], raw_unit[kPmMaxStages];
     alignas(16) float alpha[kPmRows], linv[kPmRows];
     // The plan: this CTA's first row tile and unit, its units, and for a row tile that
     // it begins, the CTAs that hold it (0: worked out from per and begin).
@@ -234,15 +234,23 @@ template <bool kFp8, int kWidth>
 struct PmSmem {
     static constexpr int kAtoms = kWidth / 64;
     static constexpr int kQAtoms = kAtoms - kPmQChannels / 64;      // of the queries, the others in tensor memory
-    // Ring slots of one unit, as many as fit beside the stages of E4M3 units.
-    static constexpr int kSlots = kFp8 ? (kWidth > DSA_KV_LORA ? 3 : 4) : (kWidth > DSA_KV_LORA ? 5 : 6);
+    // Ring slots of one unit, as many as fit beside the stages of E4M3 units. Those are the
+    // bytes in flight: four where HBM is to be kept busy, but with rotated channels only three
+    // slots fit beside them, and the fourth slot is worth more (33 requests behind 4100 tokens
+    // 45.1 -> 41.2 us; without rotation 64 ragged requests 253 -> 270 us).
+    static constexpr int kSlots = kFp8 ? 4 : (kWidth > DSA_KV_LORA ? 5 : 6);
+    static constexpr int kStages = kWidth > DSA_KV_LORA ? 2 : 4;
+    // Fetchers and wideners take alternate units. An even number of stages keeps a stage with
+    // one of either; with an odd one, a stage's next fetch could come to wait for the release
+    // of its second last unit before that of the last but two, which a parity cannot tell apart.
+    static_assert(kStages % 2 == 0 && kStages <= kPmMaxStages, "stages");
     static constexpr uint32_t kQ = 0;                               // kQAtoms x [64 rows x 128 B]
     static constexpr uint32_t kKV = kQAtoms * kPmRows * 128;        // slots x kAtoms x [32 rows x 128 B]
     static constexpr uint32_t kSlot = kAtoms * kPmAtom;
     static constexpr uint32_t kP = kKV + kSlots * kSlot;
     static constexpr uint32_t kRaw = kP + kPmPBytes;                // stages x [32 rows x kWidth B]
     static constexpr uint32_t kStage = kPmTile * kWidth;
-    static constexpr uint32_t kCtl = kRaw + (kFp8 ? kPmStages * kStage : 0);
+    static constexpr uint32_t kCtl = kRaw + (kFp8 ? kStages * kStage : 0);
     static constexpr int kBytes = (int)kCtl + (int)sizeof(PmCtl) + 1024;   // + alignment slack
 };
 static_assert(PmSmem<false, 576>::kBytes <= 232448 && PmSmem<false, 512>::kBytes <= 232448 &&
@@ -542,7 +550,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                   MergeEntry *__restrict__ merge, __nv_bfloat16 *__restrict__ out,
                   float *__restrict__ lse) {
     using S = PmSmem<kFp8, kWidth>;
-    constexpr int kAtoms = S::kAtoms, kPmSlots = S::kSlots;
+    constexpr int kAtoms = S::kAtoms, kPmSlots = S::kSlots, kPmStages = S::kStages;
     extern __shared__ uint8_t pm_smem_raw[];
     const uint32_t raw = smem_u32(pm_smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;           // 128B-swizzle atoms need 1 KB
