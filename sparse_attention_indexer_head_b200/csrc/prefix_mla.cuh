@@ -83,7 +83,7 @@ constexpr int kPmTile = 32;                           // tokens of a unit: one S
 constexpr int kPmRows = 64;                           // (query, head) rows of a row tile
 constexpr int kPmGrid = 148;                          // persistent CTAs, one per SM
 constexpr int kPmMinUnits = 2;                        // units a CTA takes at least
-constexpr int kPmPartUnits = 5;                       // units that a further part of a CTA costs
+constexpr int kPmPartUnits = 8;                       // units that a further part of a CTA costs
 // Threads: 4 softmax warps, 8 loaders, the S and PV issuers, and a second S issuer for bf16,
 // two fetchers for E4M3.
 constexpr int pm_threads(bool fp8) { return fp8 ? 512 : 480; }
