@@ -23,9 +23,9 @@
 // cycle, which for tiles of 64 rows takes 1075 cycles a unit with rope (S 24 x 16.4 + 12 x
 // 24.5, PV 8 x 48.5), and the copies write it too. A unit takes about 1300 cycles, in E4M3
 // 1800 (the codes pass through shared memory once more and are widened there). 64 requests
-// of 128 heads behind 16384 tokens take 372 to 389 us, 0.79 PFLOP/s at the 1.6 GHz that the
-// power cap leaves; 64 ragged E4M3 requests up to 32768 tokens 268 us. A request of one row
-// tile over 131072 tokens is bound by HBM instead (4 of them 121 us, 4.4 TB/s). Short calls
+// of 128 heads behind 16384 tokens take 367 to 384 us, 0.8 PFLOP/s at the 1.6 GHz that the
+// power cap leaves; 64 ragged E4M3 requests up to 32768 tokens 259 us. A request of one row
+// tile over 131072 tokens is bound by HBM instead (4 of them 108 to 123 us, 4.4 to 5 TB/s). Short calls
 // are bound by latencies: 2.5 us from the lengths to the plan, 1 to the first page-table
 // lookups, 2 to 4 for the first units (every SM's ring fills at once: 24 MB), 1.5 to the
 // first weights; behind the last product 3 us for a part's 128 KB and 6 for the second
