@@ -329,3 +329,13 @@ def test_plans(lib, requests, hm, lo, hi):
 def test_a_long_request_among_short_ones(lib):
     for hm in (16, 64):
         Batch(25, [3, 9000, 1, 40] + [5] * 200, prefix=0, page=64, hm=hm, rope=0).run_and_check(lib)
+
+
+@pytest.mark.parametrize("rope", [0, 64])
+@pytest.mark.parametrize("page", [24, 64])
+def test_fp8_ring_over_many_row_tiles(lib, page, rope):
+    # more row tiles than CTAs: a CTA's stages and slots turn over across parts of many lengths,
+    # among them requests without a token of their own
+    rng = np.random.default_rng(rope + page)
+    own = [int(x) for x in rng.integers(0, 700, 90)]
+    Batch(27, own, prefix=100, page=page, hm=128, rope=rope, fp8=True).run_and_check(lib)
