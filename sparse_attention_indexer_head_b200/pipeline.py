@@ -343,6 +343,13 @@ class StreamedDecode:
         return self.steps[0].kernels_per_step()
 
 
+def _operand(x: torch.Tensor, device: torch.device, dtype: torch.dtype) -> torch.Tensor:
+    """x as the entry points read it: of that type, on the device, its elements in order from a
+    16-byte aligned address (x itself where it is so already)."""
+    x = x.to(device, dtype).contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 class PrefixDecode:
     """Dense MLA over a paged latent cache for a batch whose requests share a prefix.
 
@@ -360,6 +367,8 @@ class PrefixDecode:
                  interleaved: bool = True, page: int = 64, fp8: bool = False, kv_scale: float = 1.0,
                  eps: float = 1e-6, sm_scale: float = KV_LORA ** -0.5, graph: bool = False,
                  device: str = "cuda"):
+        if norm_w is not None and tuple(norm_w.shape) != (KV_LORA,):
+            raise ValueError(f"norm_w is {tuple(norm_w.shape)}, not ({KV_LORA},)")
         self.device = torch.device(device)
         self.requests, self.heads, self.page, self.prefix_len = requests, heads, page, prefix_len
         self.rope = 0 if cos_sin is None else int(cos_sin.shape[1])
@@ -368,8 +377,8 @@ class PrefixDecode:
         self.interleaved, self.graph = interleaved, graph
         self.max_len = prefix_len + max_own
         dev = dict(device=self.device)
-        self.norm_w = None if norm_w is None else norm_w.to(self.device, torch.bfloat16)
-        self.cos_sin = None if cos_sin is None else cos_sin.to(self.device, torch.float32).contiguous()
+        self.norm_w = None if norm_w is None else _operand(norm_w, self.device, torch.bfloat16)
+        self.cos_sin = None if cos_sin is None else _operand(cos_sin, self.device, torch.float32)
         if self.cos_sin is not None and self.cos_sin.shape[0] < self.max_len:
             raise ValueError("cos_sin has fewer positions than the sequences may come to hold")
         # pages: the prefix's, then each request's own from the page that the prefix ends in

@@ -396,3 +396,19 @@ def test_pipeline_prefix_decode_refuses_other_shapes(lib):
     dec.fill_prefix(torch.ones(4, 1024, **bf)[:, 512:])
     torch.cuda.synchronize()
     assert (dec.cache[:4] == 1).all()
+
+
+def test_pipeline_prefix_decode_norm_weights_of_any_layout(lib):
+    """Norm weights that are a column of a packed matrix, or begin off a 16-byte border, give the
+    rows that their contiguous copy gives."""
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    g = torch.Generator(device="cuda").manual_seed(3)
+    packed = (1 + 0.1 * torch.randn(512, 8, generator=g, device="cuda")).to(torch.bfloat16)
+    flat = packed.reshape(-1)
+    x = torch.randn(5, 512, generator=g, device="cuda").to(torch.bfloat16)
+    for w in [packed[:, 3], flat[5:517], flat[1:1537:3], packed[:, 2].float()]:
+        got, want = (PrefixDecode(1, 16, 4, 5, norm_w=v) for v in (w, w.contiguous().clone()))
+        for dec in (got, want):
+            dec.fill_prefix(x)
+        torch.cuda.synchronize()
+        assert torch.equal(got.cache.view(torch.uint8), want.cache.view(torch.uint8))

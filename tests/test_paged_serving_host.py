@@ -172,3 +172,29 @@ def test_every_launching_entry_point_has_a_fast_call(B):
                "dsa_sparse_mla_workspace_size", "dsa_sparse_mla_launch_count", "dsa_noalloc_scratch_bytes",
                "dsa_prefix_mla_workspace_size"}
     assert {n for n in dir(B._call) if n.startswith("dsa_")} == set(B.EXPORTS) - queries
+
+
+def _refused(**kw):
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    a = dict(requests=2, heads=16, max_own=8, prefix_len=4, norm_w=None)
+    a.update(kw)
+    with pytest.raises(ValueError):
+        PrefixDecode(a.pop("requests"), a.pop("heads"), a.pop("max_own"), a.pop("prefix_len"), **a)
+
+
+def test_prefix_decode_refuses_norm_weights_of_another_shape(B):
+    import torch
+    for shape in [(256,), (511,), (513,), (1, 512), (512, 1), ()]:
+        _refused(norm_w=torch.ones(shape), device="cpu")
+        _refused(norm_w=torch.ones(shape, dtype=torch.bfloat16), device="cpu")
+
+
+def test_operands_are_dense_and_aligned(B):
+    import torch
+    from sparse_attention_indexer_head_b200.pipeline import _operand
+    wide = torch.arange(2048, dtype=torch.float32).to(torch.bfloat16)
+    for x in [wide[::2], wide[:1024:2], wide.view(2, 1024).t()[:512, 1], wide[3:515], wide[1:].view(-1)[:512], wide[:512]]:
+        y = _operand(x, torch.device("cpu"), torch.bfloat16)
+        assert torch.equal(x, y) and y.is_contiguous() and y.data_ptr() % 16 == 0
+    x = wide[8:520]                                       # usable as it lies: no copy
+    assert _operand(x, torch.device("cpu"), torch.bfloat16).data_ptr() == x.data_ptr()
