@@ -24,6 +24,7 @@ from .workloads import INDEX_DIM, INDEX_HEADS, KV_LORA, Workload
 QUERY_INPUTS = ("hidden", "q_idx", "q_mla", "q_req", "q_pos")
 INDEXER_MAX_POOLS = 32768          # dsa_indexer_select's pool limit
 AUTO_FUSED_MAX_QUERIES = 256       # "auto": the fused indexer up to this many queries
+PREFIX_MAX_QUERIES = 65535         # dsa_prefix_mla_decode_paged's query limit
 
 
 def _bf16(a: np.ndarray) -> torch.Tensor:
@@ -369,29 +370,31 @@ class PrefixDecode:
                  device: str = "cuda"):
         if norm_w is not None and tuple(norm_w.shape) != (KV_LORA,):
             raise ValueError(f"norm_w is {tuple(norm_w.shape)}, not ({KV_LORA},)")
+        if min(requests, max_own, prefix_len) < 0 or page < 1:
+            raise ValueError("requests, max_own and prefix_len are not negative, page is positive")
+        self.max_len = prefix_len + max_own
+        if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.shape[0] < self.max_len):
+            raise ValueError("cos_sin is a table with a row for every position that the sequences may come to hold")
         self.device = torch.device(device)
         self.requests, self.heads, self.page, self.prefix_len = requests, heads, page, prefix_len
         self.rope = 0 if cos_sin is None else int(cos_sin.shape[1])
         self.width = KV_LORA + self.rope
         self.fp8, self.kv_scale, self.eps, self.sm_scale = fp8, kv_scale, eps, sm_scale
         self.interleaved, self.graph = interleaved, graph
-        self.max_len = prefix_len + max_own
+        n_prefix, whole, n_all = -(-prefix_len // page), prefix_len // page, -(-self.max_len // page)
+        own = n_all - whole
+        self.kv_rows = (n_prefix + requests * own) * page
+        self._refuse(n_prefix, n_all, 0 if cos_sin is None else cos_sin.shape[0])
         dev = dict(device=self.device)
         self.norm_w = None if norm_w is None else _operand(norm_w, self.device, torch.bfloat16)
         self.cos_sin = None if cos_sin is None else _operand(cos_sin, self.device, torch.float32)
-        if self.cos_sin is not None and self.cos_sin.shape[0] < self.max_len:
-            raise ValueError("cos_sin has fewer positions than the sequences may come to hold")
         # pages: the prefix's, then each request's own from the page that the prefix ends in
-        n_prefix, whole = -(-prefix_len // page), prefix_len // page
-        n_all = -(-self.max_len // page)
-        own = n_all - whole
         pages = torch.arange(n_prefix + requests * own, dtype=torch.int32)
         self.prefix_table = pages[:max(1, n_prefix)].contiguous().to(self.device)
         table = torch.full((requests, max(1, n_all)), -1, dtype=torch.int32)
         if own:
             table[:, whole:] = pages[n_prefix:].view(requests, own)
         self.block_table = table.to(self.device)
-        self.kv_rows = pages.numel() * page
         self.cache = torch.zeros(self.kv_rows, self.width, dtype=torch.uint8 if fp8 else torch.bfloat16, **dev)
         i32 = dict(dtype=torch.int32, device=self.device)
         self.prefix_tokens = torch.tensor([prefix_len], **i32)
@@ -407,6 +410,19 @@ class PrefixDecode:
         self.ws = torch.empty(max(16, B.dsa_prefix_mla_workspace_size(requests, heads)), dtype=torch.uint8, **dev)
         self.tokens = 0                       # own tokens of every request so far
         self._captured = None
+
+    def _refuse(self, n_prefix: int, n_all: int, positions: int) -> None:
+        """What the calls of a step would refuse, before anything is allocated: the entry points
+        check a call's sizes and scales before they find that it has nothing to do."""
+        scale = (self.kv_scale,) if self.fp8 else ()
+        append = B.dsa_latent_append_paged_fp8 if self.fp8 else B.dsa_latent_append_paged
+        attend = B.dsa_prefix_mla_decode_paged_fp8 if self.fp8 else B.dsa_prefix_mla_decode_paged
+        if self.requests > PREFIX_MAX_QUERIES:
+            raise ValueError(f"{self.requests} requests: a step takes at most {PREFIX_MAX_QUERIES}")
+        append(None, self.width, None, self.eps, None, positions, int(self.interleaved), None, None, 0, KV_LORA, self.rope,
+               None, self.requests, n_all, self.page, None, *scale, self.kv_rows)
+        attend(None, None, *scale, self.kv_rows, None, n_prefix, None, None, n_all, self.page, None, None, None, 0,
+               self.requests, self.heads, KV_LORA, self.rope, self.sm_scale, None, None, None, 0)
 
     def _append(self, kv_new, tok_req, tok_pos, table, n_req, q=None, stream=None):
         cs, queries = self.cos_sin, ()

@@ -198,3 +198,27 @@ def test_operands_are_dense_and_aligned(B):
         assert torch.equal(x, y) and y.is_contiguous() and y.data_ptr() % 16 == 0
     x = wide[8:520]                                       # usable as it lies: no copy
     assert _operand(x, torch.device("cpu"), torch.bfloat16).data_ptr() == x.data_ptr()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(heads=0), dict(heads=24), dict(heads=144), dict(sm_scale=float("nan")), dict(sm_scale=3e38), dict(eps=-1.0),
+    dict(eps=float("inf")), dict(fp8=True, kv_scale=0.0), dict(fp8=True, kv_scale=1e-39), dict(fp8=True, kv_scale=float("inf")),
+    dict(fp8=True, kv_scale=1e30, sm_scale=1e30), dict(rope=32), dict(rope=128), dict(max_own=1 << 31, requests=1),
+])
+def test_prefix_decode_refuses_at_once_what_its_calls_refuse(B, kw):
+    import torch
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    a = dict(requests=2, heads=16, max_own=8, prefix_len=4, norm_w=None)
+    a.update(kw)
+    if "rope" in a:
+        a["cos_sin"] = torch.zeros(64, a.pop("rope"))
+    with pytest.raises(B.DsaError) as e:
+        PrefixDecode(a.pop("requests"), a.pop("heads"), a.pop("max_own"), a.pop("prefix_len"), **a)
+    assert e.value.status in (B.DSA_ERR_INVALID_ARG, B.DSA_ERR_UNSUPPORTED)
+
+
+def test_prefix_decode_refuses_sizes(B):
+    import torch
+    for kw in [dict(requests=-1), dict(max_own=-1), dict(prefix_len=-1), dict(page=0), dict(page=-16), dict(requests=65536),
+               dict(cos_sin=torch.zeros(11, 64)), dict(cos_sin=torch.zeros(64)), dict(cos_sin=torch.zeros(64, 32, 2))]:
+        _refused(**kw)
