@@ -477,17 +477,26 @@ class PrefixDecode:
         self.q.copy_(q, non_blocking=True)
         self.seq_len += 1
         self.q_pos += 1
+        try:
+            self._launch(q)
+        except BaseException:
+            self.seq_len -= 1                 # the step was not taken: the next one is for the same token
+            self.q_pos -= 1
+            raise
         self.tokens += 1
+        return self.out
+
+    def _launch(self, q: torch.Tensor) -> None:
         if not self.graph:
             self._calls()
-        else:
-            if self._captured is None:
-                self._calls()                                  # sets kernel attributes eagerly
-                # the eager step rotated q in place: the replay below starts from the caller's
-                self.q.copy_(q, non_blocking=True)
-                torch.cuda.synchronize(self.device)
-                self._captured = torch.cuda.CUDAGraph()
-                with torch.cuda.graph(self._captured):
-                    self._calls()
-            self._captured.replay()
-        return self.out
+            return
+        if self._captured is None:
+            self._calls()                                  # sets kernel attributes eagerly
+            # the eager step rotated q in place: the replay below starts from the caller's
+            self.q.copy_(q, non_blocking=True)
+            torch.cuda.synchronize(self.device)
+            captured = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(captured):
+                self._calls()
+            self._captured = captured
+        self._captured.replay()

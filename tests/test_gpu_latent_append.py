@@ -412,3 +412,40 @@ def test_pipeline_prefix_decode_norm_weights_of_any_layout(lib):
             dec.fill_prefix(x)
         torch.cuda.synchronize()
         assert torch.equal(got.cache.view(torch.uint8), want.cache.view(torch.uint8))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("name", ["dsa_latent_append_paged", "dsa_prefix_mla_decode_paged"])
+def test_pipeline_prefix_decode_after_a_call_that_was_refused(lib, monkeypatch, name, graph):
+    """A step whose call fails is not taken: the object's lengths stay, and the next step gives
+    what it gives on an object that never failed. With a graph the refusal comes at the
+    captured call, the second of the step."""
+    from sparse_attention_indexer_head_b200 import pipeline
+    rng = np.random.default_rng(9)
+    cs = torch.from_numpy(cos_sin_table(32))
+    x = to_bf16(bf16_round(rng.standard_normal((7, 576))))
+    steps = [(to_bf16(bf16_round(rng.standard_normal((2, 576)))), to_bf16(bf16_round(rng.standard_normal((2, 16, 576)))))
+             for _ in range(3)]
+    made = [pipeline.PrefixDecode(2, 16, 3, 7, norm_w=None, cos_sin=cs, graph=graph) for _ in range(2)]
+    for dec in made:
+        dec.fill_prefix(x)
+    call, count = getattr(pipeline.B, name), [0]
+
+    def refuse(*a, **kw):
+        count[0] += 1
+        if count[0] > int(graph):
+            raise lib.DsaError(name, lib.DSA_ERR_UNSUPPORTED, "refused")
+        call(*a, **kw)
+
+    with monkeypatch.context() as m:
+        m.setattr(pipeline.B, name, refuse)
+        with pytest.raises(lib.DsaError):
+            made[0].step(*steps[0])
+    assert made[0].tokens == 0 and made[0].seq_len.tolist() == [7, 7] and made[0].q_pos.tolist() == [6, 6]
+    for s in steps:
+        got, want = [dec.step(*s).clone() for dec in made]
+        assert torch.equal(got, want)
+    assert lib.dsa_device_status(reset=True) == 0
+    for dec in made:
+        assert dec.tokens == 3 and dec.seq_len.tolist() == [10, 10]
+    assert torch.equal(made[0].cache, made[1].cache)
