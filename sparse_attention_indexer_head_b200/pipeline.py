@@ -478,7 +478,7 @@ class PrefixDecode:
         self.seq_len += 1
         self.q_pos += 1
         try:
-            self._launch(q)
+            self._launch()
         except BaseException:
             self.seq_len -= 1                 # the step was not taken: the next one is for the same token
             self.q_pos -= 1
@@ -486,14 +486,15 @@ class PrefixDecode:
         self.tokens += 1
         return self.out
 
-    def _launch(self, q: torch.Tensor) -> None:
+    def _launch(self) -> None:
         if not self.graph:
             self._calls()
             return
         if self._captured is None:
+            before = self.q.clone()
             self._calls()                                  # sets kernel attributes eagerly
-            # the eager step rotated q in place: the replay below starts from the caller's
-            self.q.copy_(q, non_blocking=True)
+            # the eager step rotated q in place: the replay below starts from what came in
+            self.q.copy_(before)
             torch.cuda.synchronize(self.device)
             captured = torch.cuda.CUDAGraph()
             with torch.cuda.graph(captured):

@@ -449,3 +449,21 @@ def test_pipeline_prefix_decode_after_a_call_that_was_refused(lib, monkeypatch, 
     for dec in made:
         assert dec.tokens == 3 and dec.seq_len.tolist() == [10, 10]
     assert torch.equal(made[0].cache, made[1].cache)
+
+
+def test_pipeline_prefix_decode_takes_its_own_buffers(lib):
+    """Inputs written straight into the object's buffers: the first step of a graph, which makes
+    its calls twice, rotates them once."""
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    rng = np.random.default_rng(10)
+    cs = torch.from_numpy(cos_sin_table(32))
+    eager, graph = [PrefixDecode(2, 16, 2, 5, norm_w=None, cos_sin=cs, graph=g) for g in (False, True)]
+    x = to_bf16(bf16_round(rng.standard_normal((5, 576))))
+    for dec in (eager, graph):
+        dec.fill_prefix(x)
+    for _ in range(2):
+        kv_new, q = to_bf16(bf16_round(rng.standard_normal((2, 576)))), to_bf16(bf16_round(rng.standard_normal((2, 16, 576))))
+        graph.kv_new.copy_(kv_new)
+        graph.q.copy_(q)
+        want = eager.step(kv_new, q)
+        assert torch.equal(graph.step(graph.kv_new, graph.q), want) and torch.equal(graph.q, eager.q)
