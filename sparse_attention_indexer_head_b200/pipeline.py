@@ -463,8 +463,9 @@ class PrefixDecode:
 
     def step(self, kv_new: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
         """One token a request: kv_new bf16 [requests, 512 + rope] as projected, q bf16 [requests,
-        heads, 512 + rope] with its last rope columns not yet rotated. Returns the output
-        [requests, heads, 512] (its buffer, overwritten by the next step)."""
+        heads, 512 + rope] with its last rope columns not yet rotated, both on the device or in
+        host memory (which has been read when the call returns). Returns the output [requests,
+        heads, 512] (its buffer, overwritten by the next step)."""
         if self.prefix_len + self.tokens >= self.max_len:
             raise ValueError("the requests' pages are full")
         self._check("kv_new", kv_new, tuple(self.kv_new.shape))
@@ -473,8 +474,9 @@ class PrefixDecode:
             return self._step(kv_new, q)
 
     def _step(self, kv_new: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
-        self.kv_new.copy_(kv_new, non_blocking=True)
-        self.q.copy_(q, non_blocking=True)
+        for mine, x in ((self.kv_new, kv_new), (self.q, q)):
+            # host memory has been read when the call returns (a caller's capture reads it at every replay)
+            mine.copy_(x, non_blocking=x.is_cuda or torch.cuda.is_current_stream_capturing())
         self.seq_len += 1
         self.q_pos += 1
         try:

@@ -467,3 +467,25 @@ def test_pipeline_prefix_decode_takes_its_own_buffers(lib):
         graph.q.copy_(q)
         want = eager.step(kv_new, q)
         assert torch.equal(graph.step(graph.kv_new, graph.q), want) and torch.equal(graph.q, eager.q)
+
+
+def test_pipeline_prefix_decode_has_read_pinned_inputs_when_it_returns(lib):
+    """Pinned inputs that are refilled at once, while the stream is still busy with earlier work."""
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    rng = np.random.default_rng(11)
+    dec, ref = [PrefixDecode(2, 16, 3, 5, norm_w=None) for _ in range(2)]
+    x = to_bf16(bf16_round(rng.standard_normal((5, 512))))
+    for d in (dec, ref):
+        d.fill_prefix(x)
+    kv_new, q = [torch.empty(*s, dtype=torch.bfloat16).pin_memory() for s in ((2, 512), (2, 16, 512))]
+    want, got = [], []
+    for _ in range(3):
+        a, b = to_bf16(bf16_round(rng.standard_normal((2, 512)))), to_bf16(bf16_round(rng.standard_normal((2, 16, 512))))
+        want.append(ref.step(a, b).clone())
+        kv_new.copy_(a)
+        q.copy_(b)
+        torch.cuda._sleep(20_000_000)              # 10 ms
+        got.append(dec.step(kv_new, q).clone())
+        kv_new.fill_(9.0)
+        q.fill_(9.0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(dec.cache, ref.cache)
