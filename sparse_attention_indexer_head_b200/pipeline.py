@@ -443,12 +443,22 @@ class PrefixDecode:
             raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)}, not bfloat16 {shape}")
 
     def fill_prefix(self, kv_new: torch.Tensor, stream=None) -> None:
-        """Append the prefix's rows: kv_new bf16 [prefix_len, 512 + rope], as projected."""
+        """Append the prefix's rows: kv_new bf16 [prefix_len, 512 + rope], as projected. On another
+        ``stream`` than the current one it runs behind the current stream's work so far, and the
+        current stream's next work behind it."""
         self._check("kv_new", kv_new, (self.prefix_len, self.width))
         if kv_new.device != self.cache.device or kv_new.stride(1) != 1:
             raise ValueError("kv_new must lie on the cache's device, the channels of a row together")
         with torch.cuda.device(self.device):
+            here = torch.cuda.current_stream()
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream)
+            apart = stream is not None and stream != here
+            if apart:
+                stream.wait_stream(here)
             self._append(kv_new, self.prefix_req, self.prefix_pos, self.prefix_table, 1, stream=stream)
+            if apart:
+                here.wait_stream(stream)
 
     def _calls(self, stream=None):
         self._append(self.kv_new, self.q_req, self.q_pos, self.block_table, self.requests, self.q, stream)

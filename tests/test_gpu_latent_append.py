@@ -489,3 +489,29 @@ def test_pipeline_prefix_decode_has_read_pinned_inputs_when_it_returns(lib):
         kv_new.fill_(9.0)
         q.fill_(9.0)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(dec.cache, ref.cache)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_pipeline_prefix_decode_filled_on_another_stream(lib, handle):
+    """The fill on a side stream runs behind what the current stream still has to do (the cache's
+    zeros, the rows themselves), and the step behind the fill."""
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    rng = np.random.default_rng(12)
+    x = to_bf16(bf16_round(rng.standard_normal((300, 512))))
+    row, q = to_bf16(bf16_round(rng.standard_normal((1, 512)))), to_bf16(bf16_round(rng.standard_normal((1, 16, 512))))
+    ref = PrefixDecode(1, 16, 4, 300, norm_w=None)
+    ref.fill_prefix(x)
+    want = ref.step(row, q)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    rows = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                  # 10 ms
+    dec = PrefixDecode(1, 16, 4, 300, norm_w=None)
+    rows.copy_(x)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(2_000_000)               # the step below must not overtake the fill
+    dec.fill_prefix(rows, stream=s.cuda_stream if handle else s)
+    got = dec.step(row, q)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(dec.cache, ref.cache)
