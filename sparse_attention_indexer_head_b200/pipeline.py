@@ -376,6 +376,8 @@ class PrefixDecode:
         if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.shape[0] < self.max_len):
             raise ValueError("cos_sin is a table with a row for every position that the sequences may come to hold")
         self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"no path on {self.device}")
         self.requests, self.heads, self.page, self.prefix_len = requests, heads, page, prefix_len
         self.rope = 0 if cos_sin is None else int(cos_sin.shape[1])
         self.width = KV_LORA + self.rope
@@ -385,6 +387,8 @@ class PrefixDecode:
         own = n_all - whole
         self.kv_rows = (n_prefix + requests * own) * page
         self._refuse(n_prefix, n_all, 0 if cos_sin is None else cos_sin.shape[0])
+        if self.device.index is None:         # the device of its tensors, whichever is current at a later call
+            self.device = torch.device("cuda", torch.cuda.current_device())
         dev = dict(device=self.device)
         self.norm_w = None if norm_w is None else _operand(norm_w, self.device, torch.bfloat16)
         self.cos_sin = None if cos_sin is None else _operand(cos_sin, self.device, torch.float32)
@@ -453,7 +457,7 @@ class PrefixDecode:
             here = torch.cuda.current_stream()
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream)
-            apart = stream is not None and stream != here
+            apart = stream is not None and stream.cuda_stream != here.cuda_stream
             if apart:
                 stream.wait_stream(here)
             self._append(kv_new, self.prefix_req, self.prefix_pos, self.prefix_table, 1, stream=stream)

@@ -515,3 +515,9 @@ def test_pipeline_prefix_decode_filled_on_another_stream(lib, handle):
     got = dec.step(row, q)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(dec.cache, ref.cache)
+
+
+def test_pipeline_prefix_decode_keeps_its_device(lib):
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    dec = PrefixDecode(1, 16, 4, 4, norm_w=None)
+    assert dec.device == dec.cache.device == torch.device("cuda", torch.cuda.current_device())

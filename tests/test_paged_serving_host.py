@@ -222,3 +222,23 @@ def test_prefix_decode_refuses_sizes(B):
     for kw in [dict(requests=-1), dict(max_own=-1), dict(prefix_len=-1), dict(page=0), dict(page=-16), dict(requests=65536),
                dict(cos_sin=torch.zeros(11, 64)), dict(cos_sin=torch.zeros(64)), dict(cos_sin=torch.zeros(64, 32, 2))]:
         _refused(**kw)
+
+
+def test_prefix_decode_is_of_one_cuda_device(B, monkeypatch):
+    """A device without a number is the current one at the time, and stays it."""
+    import torch
+    from sparse_attention_indexer_head_b200 import pipeline
+    _refused(device="cpu")
+    _refused(device="meta")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    seen = []
+
+    def stop(x, device, dtype):
+        seen.append(device)
+        raise KeyError                                     # before anything is allocated
+
+    monkeypatch.setattr(pipeline, "_operand", stop)
+    for device in ("cuda", "cuda:1"):
+        with pytest.raises(KeyError):
+            pipeline.PrefixDecode(1, 16, 4, 4, norm_w=torch.ones(512), device=device)
+    assert seen == [torch.device("cuda", 3), torch.device("cuda", 1)]
