@@ -446,6 +446,7 @@ class PrefixDecode:
         if tuple(x.shape) != shape or x.dtype != torch.bfloat16:
             raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)}, not bfloat16 {shape}")
 
+    @torch.no_grad()
     def fill_prefix(self, kv_new: torch.Tensor, stream=None) -> None:
         """Append the prefix's rows: kv_new bf16 [prefix_len, 512 + rope], as projected. On another
         ``stream`` than the current one it runs behind the current stream's work so far, and the
@@ -475,6 +476,7 @@ class PrefixDecode:
         else:
             B.dsa_prefix_mla_decode_paged(self.q, self.cache, self.kv_rows, *where)
 
+    @torch.no_grad()
     def step(self, kv_new: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
         """One token a request: kv_new bf16 [requests, 512 + rope] as projected, q bf16 [requests,
         heads, 512 + rope] with its last rope columns not yet rotated, both on the device or in

@@ -521,3 +521,19 @@ def test_pipeline_prefix_decode_keeps_its_device(lib):
     from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
     dec = PrefixDecode(1, 16, 4, 4, norm_w=None)
     assert dec.device == dec.cache.device == torch.device("cuda", torch.cuda.current_device())
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_pipeline_prefix_decode_keeps_no_autograd_history(lib, graph):
+    """Inputs that come out of layers with gradients on: the object's buffers hold none of it."""
+    from sparse_attention_indexer_head_b200.pipeline import PrefixDecode
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    dec, ref = [PrefixDecode(2, 16, 3, 4, norm_w=torch.nn.Parameter(torch.ones(512, **bf)), graph=graph) for _ in range(2)]
+    x, kv_new, q = torch.randn(4, 512, **bf), torch.randn(2, 512, **bf), torch.randn(2, 16, 512, **bf)
+    scale = torch.nn.Parameter(torch.ones((), **bf))
+    dec.fill_prefix(x * scale)
+    ref.fill_prefix(x)
+    for _ in range(2):
+        got, want = dec.step(kv_new * scale, q * scale), ref.step(kv_new, q)
+        assert torch.equal(got, want) and not got.requires_grad
+    assert not any(t.requires_grad for t in (dec.kv_new, dec.q, dec.out, dec.lse, dec.cache))
