@@ -539,7 +539,10 @@ int dsa_latent_append_paged_fp8(const dsa_bf16 *kv_new, int64_t kv_new_stride,
  * Requires kv_lora == 512, rope_dim 0 or 64, Hm a multiple of 16 with 16 <= Hm
  * <= 128, Q <= 65535, kv_rows <= INT32_MAX (DSA_ERR_UNSUPPORTED otherwise),
  * page_size >= 1, prefix_blocks and max_blocks >= 0, sm_scale * log2(e) finite
- * in fp32 (DSA_ERR_INVALID_ARG).
+ * in fp32 (DSA_ERR_INVALID_ARG). Tables that name up to 2^26 tokens a sequence
+ * (the larger of prefix_blocks and max_blocks, times page_size) are always taken;
+ * longer ones are DSA_ERR_UNSUPPORTED where the call's work could pass its 32-bit
+ * counts: 2^30 tokens for 128 queries of 16 heads, 2^31 for about 4700 of 64.
  * Q == 0 launches nothing. Nothing is read before the wait on the preceding
  * kernel.
  */

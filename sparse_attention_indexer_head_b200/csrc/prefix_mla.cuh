@@ -369,7 +369,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
             w.load(g, rt, tid, P);
             units = w.units;
         }
-        inc = warp_inclusive_sum((unsigned)units, lane);   // of 32 tiles of at most 2^26 units
+        inc = warp_inclusive_sum((unsigned)units, lane);   // fits: pm_sums_fit
         if (lane == 31) ctl->warp_sum[warp] = inc;
         if (tid == 0) ctl->count = ctl->parts = 0;
         __syncthreads();
@@ -470,7 +470,7 @@ DSA_DEVINL void pm_plan(PmCtl *ctl, void *scratch, const PrefixGeom &g, const Ro
             ctl->first = w;
             ctl->first_unit = (int)(begin - first);
             ctl->first_units = units;
-            ctl->count = (int)min((long long)INT32_MAX, min(per, total - begin));
+            ctl->count = (int)min(per, total - begin);
         }
     }
     tc::fence_proxy_async_smem();                     // the scratch becomes the ring
@@ -1425,6 +1425,15 @@ inline size_t prefix_mla_workspace_bytes(int Q, int Hm) {
     return Q > 0 && Hm > 0 ? kPmPartBytes + kPmMlBytes + kPmGrid * sizeof(MergeEntry) : 0;
 }
 
+// Whether pm_plan's sums hold whatever the lengths on the device turn out to be: the units of
+// 32 row tiles in 32 bits, a CTA's share in an int. A tile walks at most its queries' sequences,
+// each of them no longer than its table's pages, and two units more a query for their ends.
+inline bool pm_sums_fit(const PrefixGeom &g, const RowTiles &rt) {
+    const long long held = std::min((long long)std::max(g.prefix_blocks, g.max_blocks) * g.page, (long long)kMaxTokens);
+    const long long tile = rt.qpt * (held / kPmTile + 2);
+    return std::min(rt.count, 32) * tile <= (long long)UINT32_MAX && rt.count * tile / kPmGrid < INT32_MAX;
+}
+
 template <bool kFp8, int kWidth>
 inline int prefix_mla_run(const void *q, const void *kv, const PrefixGeom &g, int Hm,
                           float scale_log2, float out_scale, void *out, float *lse, void *ws,
@@ -1480,7 +1489,8 @@ inline int prefix_mla_launch(const void *q, const void *kv, float kv_scale, int6
     if (kv_lora != DSA_KV_LORA || (rope != 0 && rope != kRopeDim) || Hm % 16 != 0 ||
         Hm > DSA_MAX_MLA_HEADS)
         return DSA_ERR_UNSUPPORTED;
-    if (kv_rows > (int64_t)INT32_MAX || g.Q > 65535) return DSA_ERR_UNSUPPORTED;
+    if (kv_rows > (int64_t)INT32_MAX || g.Q > 65535 || !pm_sums_fit(g, RowTiles(g.Q, Hm)))
+        return DSA_ERR_UNSUPPORTED;
     if (g.Q == 0) return DSA_OK;
     if (!q || !g.q_req || !g.q_pos || !out || (kv_rows > 0 && !kv) || (g.B > 0 && !g.seq_len) ||
         (g.B > 0 && g.max_blocks > 0 && !g.block_table) ||

@@ -242,3 +242,27 @@ def test_prefix_decode_is_of_one_cuda_device(B, monkeypatch):
         with pytest.raises(KeyError):
             pipeline.PrefixDecode(1, 16, 4, 4, norm_w=torch.ones(512), device=device)
     assert seen == [torch.device("cuda", 3), torch.device("cuda", 1)]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefix_mla_tables_too_long_for_the_plan(B, fp8):
+    """Work beyond the plan's counts (32 row tiles' units of 32 tokens in 32 bits, a CTA's in 31) is
+    refused; a call that is not goes on to the workspace check, never to a launch."""
+    def status(tokens, Q, Hm, at="mb"):
+        page = next(p for p in (1 << 20, 1 << 16, 1) if tokens % p == 0)
+        return _mla(B, fp8, **{at: tokens // page}, page=page, Q=Q, B=Q, Hm=Hm, ws=None)
+
+    for Q, Hm, most in [(128, 16, (1 << 30) - 128), (65535, 64, 1 << 26), (65535, 128, 1 << 26), (65535, 16, 1 << 26),
+                        (96, 32, (1 << 31) - 1), (4000, 64, (1 << 31) - 1), (1, 16, (1 << 31) - 1), (124, 16, 1 << 30)]:
+        for at in ("mb", "pb"):
+            assert status(most, Q, Hm, at) == B.DSA_ERR_WORKSPACE, (Q, Hm, most)
+    for Q, Hm, tokens in [(128, 16, 1 << 30), (128, 16, (1 << 31) - 1), (5000, 64, (1 << 31) - 1), (65535, 128, 1 << 28),
+                          (65535, 16, 1 << 29)]:
+        for at in ("mb", "pb"):
+            assert status(tokens, Q, Hm, at) == B.DSA_ERR_UNSUPPORTED, (Q, Hm, tokens)
+    # what the bound stands for: tiles of qpt queries, each over the whole of its table
+    for Q, Hm, tokens in [(128, 16, (1 << 30) - 128), (65535, 128, 1 << 26), (65535, 16, 1 << 26), (96, 32, (1 << 31) - 65)]:
+        qpt = max(1, 64 // Hm) if Hm < 64 else 1
+        tiles = -(-Q // qpt) if qpt > 1 else Q * -(-Hm // 64)
+        tile = qpt * (tokens // 32 + 1) + 1
+        assert min(32, tiles) * tile < 1 << 32 and -(-tiles * tile // 148) < 1 << 31
