@@ -172,7 +172,7 @@ def dsa_kpool_compress(k, gate, tok_valid, req_start, B: int, D: int, kpool: int
                        stream=None) -> None:
     _check("dsa_kpool_compress", _call.dsa_kpool_compress(
         k, gate, tok_valid, req_start, B, D, kpool, max_pools, ape,
-        ln_w, ln_b, eps, pool_keys, pool_idx, pool_valid,
+        ln_w, ln_b, float(eps), pool_keys, pool_idx, pool_valid,
         first_valid, _stream(stream)))
 
 
@@ -188,7 +188,7 @@ def dsa_kpool_compress_tokens(k, gate, tok_valid, req_start, B: int, D: int, kpo
                               pool_keys, pool_idx, pool_valid, first_valid, stream=None) -> None:
     _check("dsa_kpool_compress_tokens", _call.dsa_kpool_compress_tokens(
         k, gate, tok_valid, req_start, B, D, kpool, max_pools, ape,
-        ln_w, ln_b, eps, tok_begin, tok_end, pool_keys,
+        ln_w, ln_b, float(eps), tok_begin, tok_end, pool_keys,
         pool_idx, pool_valid, first_valid, _stream(stream)))
 
 
@@ -239,8 +239,8 @@ def dsa_sparse_mla_decode(q, kv, kv_rows: int, req_start, q_req, token_ids, Q: i
                           Hm: int, W: int, kv_lora: int, rope_dim: int, sm_scale: float, out, lse,
                           workspace, workspace_bytes: int, stream=None) -> None:
     _check("dsa_sparse_mla_decode", _call.dsa_sparse_mla_decode(
-        q, kv, kv_rows, req_start, q_req, token_ids, Q, B, Hm, W, kv_lora,
-        rope_dim, sm_scale, out, lse, workspace, workspace_bytes,
+        q, kv, int(kv_rows), req_start, q_req, token_ids, Q, B, Hm, W, kv_lora,
+        rope_dim, float(sm_scale), out, lse, workspace, int(workspace_bytes),
         _stream(stream)))
 
 
@@ -250,8 +250,8 @@ def dsa_sparse_mla_decode_noalloc(q, kv, kv_rows: int, req_start, q_req, token_i
     """dsa_sparse_mla_decode for callers that cannot allocate: the split-KV scratch is the
     library's own static device area (see include/dsa.h)."""
     _check("dsa_sparse_mla_decode_noalloc", _call.dsa_sparse_mla_decode_noalloc(
-        q, kv, kv_rows, req_start, q_req, token_ids, Q, B, Hm, W, kv_lora,
-        rope_dim, sm_scale, out, lse, _stream(stream)))
+        q, kv, int(kv_rows), req_start, q_req, token_ids, Q, B, Hm, W, kv_lora,
+        rope_dim, float(sm_scale), out, lse, _stream(stream)))
 
 
 def dsa_sparse_mla_decode_paged(q, kv, kv_rows: int, block_table, max_blocks: int, page_size: int,
@@ -260,7 +260,7 @@ def dsa_sparse_mla_decode_paged(q, kv, kv_rows: int, block_table, max_blocks: in
                                 workspace_bytes: int, stream=None) -> None:
     _check("dsa_sparse_mla_decode_paged", _call.dsa_sparse_mla_decode_paged(
         q, kv, kv_rows, block_table, max_blocks, page_size, seq_len,
-        q_req, token_ids, Q, B, Hm, W, kv_lora, rope_dim, sm_scale, out,
+        q_req, token_ids, Q, B, Hm, W, kv_lora, rope_dim, float(sm_scale), out,
         lse, workspace, workspace_bytes, _stream(stream)))
 
 
@@ -270,9 +270,9 @@ def dsa_sparse_mla_decode_paged_fp8(q, kv8, kv_scale: float, kv_rows: int, block
                                     sm_scale: float, out, lse, workspace, workspace_bytes: int,
                                     stream=None) -> None:
     _check("dsa_sparse_mla_decode_paged_fp8", _call.dsa_sparse_mla_decode_paged_fp8(
-        q, kv8, kv_scale, kv_rows, block_table, max_blocks, page_size,
+        q, kv8, float(kv_scale), kv_rows, block_table, max_blocks, page_size,
         seq_len, q_req, token_ids, Q, B, Hm, W, kv_lora, rope_dim,
-        sm_scale, out, lse, workspace, workspace_bytes, _stream(stream)))
+        float(sm_scale), out, lse, workspace, workspace_bytes, _stream(stream)))
 
 
 def dsa_latent_append_paged(kv_new, kv_new_stride: int, norm_w, eps: float, cos_sin, max_pos: int,

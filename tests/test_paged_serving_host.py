@@ -266,3 +266,22 @@ def test_prefix_mla_tables_too_long_for_the_plan(B, fp8):
         tiles = -(-Q // qpt) if qpt > 1 else Q * -(-Hm // 64)
         tile = qpt * (tokens // 32 + 1) + 1
         assert min(32, tiles) * tile < 1 << 32 and -(-tiles * tile // 148) < 1 << 31
+
+
+def test_calls_convert_numbers_as_before(B):
+    """Row counts and workspace sizes given as floats, scales as anything that float() takes: calls
+    that launch nothing (no query, no request) get through, refusals keep their status."""
+    for rows, size in [(64, 4096), (64.0, 4096.0), (np.float64(64), np.int64(4096)), ("64", "4096")]:
+        for sm in (0.1, "0.1", np.float32(0.1)):
+            B.dsa_sparse_mla_decode(FAKE, FAKE, rows, FAKE, FAKE, FAKE, 0, 1, 16, 48, 512, 0, sm, FAKE, None, FAKE, size, 0)
+            B.dsa_sparse_mla_decode_noalloc(FAKE, FAKE, rows, FAKE, FAKE, FAKE, 0, 1, 16, 48, 512, 0, sm, FAKE, None, 0)
+    for sm in (0.1, "0.1", np.float32(0.1)):
+        B.dsa_sparse_mla_decode_paged(FAKE, FAKE, 64, FAKE, 2, 16, FAKE, FAKE, FAKE, 0, 1, 16, 48, 512, 0, sm, FAKE, None, FAKE, 0, 0)
+        B.dsa_sparse_mla_decode_paged_fp8(FAKE, FAKE, sm, 64, FAKE, 2, 16, FAKE, FAKE, FAKE, 0, 1, 16, 48, 512, 0, sm, FAKE, None,
+                                          FAKE, 0, 0)
+    for eps in ("nan", "-1", -1):
+        with pytest.raises(B.DsaError):
+            B.dsa_kpool_compress(FAKE, FAKE, FAKE, FAKE, 2, 128, 4, 8, FAKE, FAKE, FAKE, eps, FAKE, FAKE, FAKE, FAKE, 0)
+        with pytest.raises(B.DsaError):
+            B.dsa_kpool_compress_tokens(FAKE, FAKE, FAKE, FAKE, 2, 128, 4, 8, FAKE, FAKE, FAKE, eps, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                        FAKE, 0)
