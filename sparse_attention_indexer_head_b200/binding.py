@@ -6,13 +6,14 @@ address or None; ``stream`` accepts a torch.cuda.Stream, an int handle or None
 (torch's current stream). A non-OK status raises DsaError. The calls that launch
 go through the extension module _dsacall, the queries through ctypes (``lib``, which
 has every entry point). There is no fallback: importing this module fails loudly
-when libdsa.so or _dsacall.so is missing.
+when libdsa.so or _dsacall (built for this interpreter) is missing.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.util
 import os
+import sysconfig
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -100,10 +101,10 @@ lib = _load()
 
 
 def _load_call():
-    path = os.path.join(HERE, "_dsacall.so")
+    path = os.path.join(HERE, "_dsacall" + sysconfig.get_config_var("EXT_SUFFIX"))
     if not os.path.exists(path):
         raise ImportError(
-            f"_dsacall.so not found at {path}; build it with "
+            f"the extension module was not found at {path}; build it with "
             "`python -m sparse_attention_indexer_head_b200.build` (no fallback exists)")
     spec = importlib.util.spec_from_file_location(__package__ + "._dsacall", path)
     module = importlib.util.module_from_spec(spec)

@@ -1,10 +1,10 @@
-"""Build libdsa.so (the C ABI of include/dsa.h) for sm_100a, in-tree, and _dsacall.so, the
-extension module through which Python calls it.
+"""Build libdsa.so (the C ABI of include/dsa.h) for sm_100a, in-tree, and _dsacall (with the
+interpreter's suffix), the extension module through which Python calls it.
 
 The library is one translation unit, csrc/dsa_abi.cu, which includes every
 stage's kernels. Compiled with nvcc for sm_100a only. The module
-(csrc/dsa_pycall.cpp) is compiled with the C++ compiler against Python's headers and
-linked to the library beside it.
+(csrc/dsa_pycall.cpp) is compiled with the C++ compiler against Python's headers, which
+must be installed, and linked to the library beside it.
 """
 from __future__ import annotations
 
@@ -18,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdsa.so")
-CALL = os.path.join(HERE, "_dsacall.so")
+# Named after the interpreter that it is built for: another one builds its own beside it.
+CALL = os.path.join(HERE, "_dsacall" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALL_SOURCE = os.path.join(CSRC, "dsa_pycall.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 CXX = os.environ.get("CXX", "g++")

@@ -285,3 +285,11 @@ def test_calls_convert_numbers_as_before(B):
         with pytest.raises(B.DsaError):
             B.dsa_kpool_compress_tokens(FAKE, FAKE, FAKE, FAKE, 2, 128, 4, 8, FAKE, FAKE, FAKE, eps, FAKE, FAKE, FAKE, FAKE, FAKE,
                                         FAKE, 0)
+
+
+def test_extension_module_is_of_this_interpreter(B):
+    """Another Python version's module has another name, so that it is not loaded."""
+    import sysconfig
+    from sparse_attention_indexer_head_b200 import build
+    assert build.CALL.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert B._call.__spec__.origin == build.CALL
