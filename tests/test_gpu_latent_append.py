@@ -406,7 +406,7 @@ def test_pipeline_prefix_decode_norm_weights_of_any_layout(lib):
     packed = (1 + 0.1 * torch.randn(512, 8, generator=g, device="cuda")).to(torch.bfloat16)
     flat = packed.reshape(-1)
     x = torch.randn(5, 512, generator=g, device="cuda").to(torch.bfloat16)
-    for w in [packed[:, 3], flat[5:517], flat[1:1537:3], packed[:, 2].float()]:
+    for w in [packed[:, 0], packed[:, 3], flat[5:517], flat[1:1537:3], packed[:, 2].float()]:
         got, want = (PrefixDecode(1, 16, 4, 5, norm_w=v) for v in (w, w.contiguous().clone()))
         for dec in (got, want):
             dec.fill_prefix(x)

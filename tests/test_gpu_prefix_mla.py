@@ -339,3 +339,34 @@ def test_fp8_ring_over_many_row_tiles(lib, page, rope):
     rng = np.random.default_rng(rope + page)
     own = [int(x) for x in rng.integers(0, 700, 90)]
     Batch(27, own, prefix=100, page=page, hm=128, rope=rope, fp8=True).run_and_check(lib)
+
+
+def block_threads(fp8):
+    """Threads of the attention's block, by the source: the plan takes a row tile a thread."""
+    import re
+    from sparse_attention_indexer_head_b200 import build
+    with open(f"{build.CSRC}/prefix_mla.cuh") as f:
+        return int(re.search(r"pm_threads\(bool fp8\) \{ return fp8 \? (\d+) : (\d+);", f.read())[1 if fp8 else 2])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hm,lo,hi", [(128, 0, 60), (64, 1, 40), (16, 0, 9)])
+def test_plans_of_more_row_tiles_than_threads(lib, hm, lo, hi, fp8):
+    tiles = block_threads(fp8) + 70
+    requests = tiles // 2 if hm == 128 else tiles if hm == 64 else 4 * tiles
+    rng = np.random.default_rng(hm + fp8)
+    own = [int(x) for x in rng.integers(lo, hi + 1, requests)]
+    own[3], own[requests // 2] = 1500, 700                  # ranges that end inside a long tile
+    Batch(requests, own, page=32, hm=hm, rope=0, fp8=fp8).run_and_check(lib)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hm,n", [(128, 300), (64, 190), (32, 130), (16, 263)])
+def test_a_prompt_chunk(lib, hm, n, fp8):
+    """Consecutive queries of one request behind a prefix, each seeing one token more than the one
+    before, and padding rows behind the last: up to 600 row tiles, or runs of queries that walk
+    together."""
+    own, P, pad = 20 + n, 75, 5
+    q_req = np.r_[np.zeros(n, int), np.full(pad, -1)]
+    q_pos = np.r_[P + own - n + np.arange(n), np.zeros(pad, int)]
+    Batch(n + hm, [own], prefix=P, page=16, hm=hm, fp8=fp8, q_req=q_req, q_pos=q_pos).run_and_check(lib)
