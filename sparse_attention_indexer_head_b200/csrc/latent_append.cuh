@@ -12,13 +12,13 @@
 // (a row is read as an operand of that type, so nothing finer would be used).
 //
 // Bound by bytes for a prompt's chunk and by the latency of one dependent chain
-// for a decode step (position -> block table -> row address; the row's loads do
-// not depend on it and go out with it). So: one warp a row, every load of the
-// row issued before the first use, and one warp for every 16 query heads of a
-// token, four 16-byte vectors a lane in flight. 48 registers keep five blocks on an SM
+// for a decode step (position -> block table -> cos and sin -> store; the row's own
+// loads depend on none of it and go out first). So: one warp a row, all of the row
+// and its weights in flight before the first use, and one warp for every 16 query
+// heads of a token, four 16-byte vectors a lane in flight. 48 registers keep five blocks on an SM
 // (40 warps: a chunk's loads are what hides its latency; six warps a block row and 64
-// registers took 8.2 us where this takes 6.7). One row and 64 rows with 64 heads 2.2 and
-// 2.6 us (the chain), 2048 tokens into E4M3 and 16336 rows of bf16 6.7 us (5.6 and 5.0
+// registers took 8.2 us where this takes 6.7). One row with 16 heads and 64 rows with 128
+// 2.1 and 2.6 us (the chain), 2048 tokens into E4M3 and 16336 rows of bf16 6.7 us (5.6 and 5.0
 // TB/s).
 #pragma once
 

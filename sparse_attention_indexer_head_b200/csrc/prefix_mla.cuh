@@ -22,12 +22,13 @@
 // What bounds it: the tensor cores read their operands from shared memory at 128 bytes a
 // cycle, which for tiles of 64 rows takes 1075 cycles a unit with rope (S 24 x 16.4 + 12 x
 // 24.5, PV 8 x 48.5), and the copies write it too. A unit takes about 1300 cycles, in E4M3
-// 1800 (the codes pass through shared memory once more and are widened there). 64 requests
+// 1800 (the codes pass through shared memory once more and are widened there): a cache of
+// half the bytes takes 5 to 40 % more time than a bf16 one of the same lengths. 64 requests
 // of 128 heads behind 16384 tokens take 367 to 384 us, 0.8 PFLOP/s at the 1.6 GHz that the
 // power cap leaves; 64 ragged E4M3 requests up to 32768 tokens 259 us. A request of one row
 // tile over 131072 tokens is bound by HBM instead (4 of them 108 to 123 us, 4.4 to 5 TB/s). Short calls
 // are bound by latencies: 2.5 us from the lengths to the plan, 1 to the first page-table
-// lookups, 2 to 4 for the first units (every SM's ring fills at once: 24 MB), 1.5 to the
+// lookups, 2 to 4 for the first units (every SM's ring fills at once: 27 to 29 MB in bf16), 1.5 to the
 // first weights; behind the last product 3 us for a part's 128 KB and 6 for the second
 // launch that merges the parts. One row of 512 tokens 11.9 us, 16 requests behind 6144 37.
 #pragma once
@@ -237,7 +238,7 @@ struct PmSmem {
     // Ring slots of one unit, as many as fit beside the stages of E4M3 units. Those are the
     // bytes in flight: four where HBM is to be kept busy, but with rotated channels only three
     // slots fit beside them, and the fourth slot is worth more (33 requests behind 4100 tokens
-    // 45.1 -> 41.2 us; without rotation 64 ragged requests 253 -> 270 us).
+    // 44.4 -> 40.8 us; without rotation 64 ragged requests 253 -> 270 us).
     static constexpr int kSlots = kFp8 ? 4 : (kWidth > DSA_KV_LORA ? 5 : 6);
     static constexpr int kStages = kWidth > DSA_KV_LORA ? 2 : 4;
     // Fetchers and wideners take alternate units. An even number of stages keeps a stage with
@@ -736,7 +737,7 @@ prefix_mla_kernel(const __grid_constant__ CUtensorMap kv_map, int box_rows,
                                               : make_uint2(0u, 0u);
             }
             // Now the codes are in registers. Two stages are released here, so that the next
-            // copies run behind the widening (4 requests of 131072 tokens with rope 145 -> 130
+            // copies run behind the widening (4 requests of 131072 tokens with rope 145 -> 129
             // us); of four it only puts the loads' latency before the wait for the slot (64
             // ragged requests 258 -> 271 us).
             constexpr bool kEarly = kPmStages == 2;

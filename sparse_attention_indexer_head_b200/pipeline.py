@@ -358,7 +358,9 @@ class PrefixDecode:
     device. ``fill_prefix`` appends the shared prefix's latent rows once; ``step`` appends
     one new row a request (normalised, rotated at its position; dsa_latent_append_paged),
     rotates the step's query heads in the same launch and attends over prefix and own
-    tokens (dsa_prefix_mla_decode_paged). With ``graph`` the two calls are captured at the
+    tokens (dsa_prefix_mla_decode_paged): all requests in step, from the prefix's end on.
+    Batches of ragged lengths, several new tokens a request or prompts of its own call the
+    two entry points themselves. A step whose call fails is not taken. With ``graph`` the two calls are captured at the
     first step and replayed: the lengths are device data, and every page a request can
     come to hold is in its table from the start.
     """
