@@ -351,6 +351,14 @@ def _operand(x: torch.Tensor, device: torch.device, dtype: torch.dtype) -> torch
     return x if x.data_ptr() % 16 == 0 else x.clone()
 
 
+def _torch_stream(s) -> torch.cuda.Stream:
+    """A stream as torch's: a handle (0 is the default stream) or an object that has one."""
+    if isinstance(s, torch.cuda.Stream):
+        return s
+    handle = s if isinstance(s, int) else s.cuda_stream
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
 class PrefixDecode:
     """Dense MLA over a paged latent cache for a batch whose requests share a prefix.
 
@@ -458,14 +466,12 @@ class PrefixDecode:
             raise ValueError("kv_new must lie on the cache's device, the channels of a row together")
         with torch.cuda.device(self.device):
             here = torch.cuda.current_stream()
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream)
-            apart = stream is not None and stream.cuda_stream != here.cuda_stream
-            if apart:
-                stream.wait_stream(here)
-            self._append(kv_new, self.prefix_req, self.prefix_pos, self.prefix_table, 1, stream=stream)
-            if apart:
-                here.wait_stream(stream)
+            side = here if stream is None else _torch_stream(stream)
+            if side.cuda_stream != here.cuda_stream:
+                side.wait_stream(here)
+            self._append(kv_new, self.prefix_req, self.prefix_pos, self.prefix_table, 1, stream=side)
+            if side.cuda_stream != here.cuda_stream:
+                here.wait_stream(side)
 
     def _calls(self, stream=None):
         self._append(self.kv_new, self.q_req, self.q_pos, self.block_table, self.requests, self.q, stream)

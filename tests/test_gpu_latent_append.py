@@ -537,3 +537,27 @@ def test_pipeline_prefix_decode_keeps_no_autograd_history(lib, graph):
         got, want = dec.step(kv_new * scale, q * scale), ref.step(kv_new, q)
         assert torch.equal(got, want) and not got.requires_grad
     assert not any(t.requires_grad for t in (dec.kv_new, dec.q, dec.out, dec.lse, dec.cache))
+
+
+def test_pipeline_prefix_decode_fills_on_the_stream_that_it_is_given(lib, monkeypatch):
+    """By handle (0: the default stream), by torch's object or by another that has a handle."""
+    from types import SimpleNamespace
+    from sparse_attention_indexer_head_b200 import pipeline
+    dec = pipeline.PrefixDecode(1, 16, 4, 4, norm_w=None)
+    x = torch.ones(4, 512, dtype=torch.bfloat16, device="cuda")
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call, seen = pipeline.B.dsa_latent_append_paged, []
+
+    def note(*a, stream):
+        seen.append(stream.cuda_stream)
+        call(*a, stream=stream)
+
+    monkeypatch.setattr(pipeline.B, "dsa_latent_append_paged", note)
+    for given in (None, 0, s, s.cuda_stream, SimpleNamespace(cuda_stream=s.cuda_stream), t):
+        with torch.cuda.stream(t):
+            dec.fill_prefix(x, stream=given)
+    dec.fill_prefix(x, stream=0)
+    torch.cuda.synchronize()
+    assert seen == [t.cuda_stream, 0, s.cuda_stream, s.cuda_stream, s.cuda_stream, t.cuda_stream, 0]
+    assert (dec.cache[:4] == 1).all()
