@@ -370,3 +370,44 @@ def test_a_prompt_chunk(lib, hm, n, fp8):
     q_req = np.r_[np.zeros(n, int), np.full(pad, -1)]
     q_pos = np.r_[P + own - n + np.arange(n), np.zeros(pad, int)]
     Batch(n + hm, [own], prefix=P, page=16, hm=hm, fp8=fp8, q_req=q_req, q_pos=q_pos).run_and_check(lib)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_largest_batch(lib, fp8):
+    """65535 queries of 128 heads, each a request of up to three tokens: outputs of 8 GB. Against
+    the formula in 64 bits on the device, with assert_attention_close's tolerances."""
+    Q, hm, rows, most, scale = 65535, 128, 4096, 3, 0.25
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    sm = float(np.float32(512 ** -0.5))
+    values = torch.randn(rows, 512, generator=gen, device="cuda")
+    cache = values.to(torch.float8_e4m3fn) if fp8 else values.to(torch.bfloat16)
+    values = cache.double() * (scale if fp8 else 1.0)
+    table = torch.randint(0, rows, (Q, most), generator=gen, device="cuda", dtype=torch.int32)
+    seq = torch.randint(0, most + 1, (Q,), generator=gen, device="cuda", dtype=torch.int32)
+    q = torch.empty(Q, hm, 512, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    out = torch.full((Q, hm, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((Q, hm), float("nan"), device="cuda")
+    ws = torch.empty(lib.dsa_prefix_mla_workspace_size(Q, hm), dtype=torch.uint8, device="cuda")
+    where = (None, 0, None, table, most, 1, seq, torch.arange(Q, dtype=torch.int32, device="cuda"), seq - 1, Q, Q, hm, 512, 0,
+             sm, out, lse, ws, ws.numel())
+    if fp8:
+        lib.dsa_prefix_mla_decode_paged_fp8(q, cache.view(torch.uint8), scale, rows, *where)
+    else:
+        lib.dsa_prefix_mla_decode_paged(q, cache, rows, *where)
+    torch.cuda.synchronize()
+    assert lib.dsa_device_status(reset=True) == 0
+    token = torch.arange(most, device="cuda")
+    for i in range(0, Q, 2048):
+        k, x, n = values[table[i:i + 2048].long()], q[i:i + 2048].double(), seq[i:i + 2048]
+        seen = (token < n[:, None])[:, None]
+        z = (x @ k.transpose(1, 2) * sm).masked_fill(~seen, -np.inf)
+        terms = (x.abs() @ k.abs().transpose(1, 2) * sm).masked_fill(~seen, 0).amax(2)
+        p = torch.where(n[:, None, None] > 0, torch.softmax(z, 2), 0.0)
+        ref, rlse, mag = p @ k, torch.logsumexp(z, 2), p @ k.abs()
+        dz = (512 + 12) * 2.0 ** -23 * terms + 2.0 ** -21
+        sums = (n[:, None] + 8) * 2.0 ** -23
+        tol = (2.0 ** -8 * ref.abs() + mag * (2.0 ** -8 + 2 * dz + 2 * sums)[..., None]) * (1 + 2.0 ** -6)
+        assert ((out[i:i + 2048].double() - ref).abs() <= tol).all()
+        got, none = lse[i:i + 2048].double(), (n == 0)[:, None].expand(-1, hm)
+        assert (torch.isneginf(got) == none).all()
+        assert ((got - rlse).abs() <= dz + sums + 2.0 ** -22 * rlse.abs())[~none].all()
